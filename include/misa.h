@@ -224,6 +224,134 @@ int dsa_index_dense(const misa_problem_t* p, const uint16_t* q, const float* w,
                     const uint16_t* K, int32_t k, int32_t* idx, float* val, float* scores_dbg,
                     int64_t scores_ld, void* ws, size_t ws_bytes, misa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The key/value cache around the indexer: writing a step's keys and values
+ * into it, and attending over it -- over every token, or over the tokens
+ * that the indexer selected (gist.science summary, "Probleemstelling": the
+ * indexer's top-k tokens are what the main attention then reads).
+ *
+ * These calls read from misa_problem_t the batch only (num_seqs,
+ * num_queries, max_seq_len, total_keys, key_offsets, query_offsets, q_pos);
+ * num_heads, head_dim, block, total_blocks and block_offsets belong to the
+ * indexer and may hold anything.  L_s = key_offsets[s+1] - key_offsets[s]
+ * tokens of sequence s are in the cache, the queries' own included.  Query
+ * rows at and behind query_offsets[S] are padding: nothing of theirs is read
+ * and their rows of every output are left as they were.
+ * ------------------------------------------------------------------------ */
+enum { MISA_BF16 = 0, MISA_FP16 = 1 };
+
+/* A cache of keys and values, num_kv_heads heads of head_dim elements a token.
+ *   Paged (page_table != NULL): token p of sequence s is row p % page_size of
+ *   page page_table[s * page_table_stride + p / page_size]; its head h starts
+ *       page * page_stride + (p % page_size) * token_stride + h * head_stride
+ *   elements behind k (and behind v).  Any order of pages, any page size, and
+ *   either order of tokens and heads in a page (the strides say which).
+ *   Packed (page_table == NULL): token p of sequence s is row
+ *   key_offsets[s] + p, token_stride elements apart: the layout of the
+ *   indexer's K.  page_size, num_pages, pages_per_seq and page_stride are
+ *   not read.
+ * k and v are 16-byte aligned; strides are multiples of 8 elements.  A page
+ * number outside 0..num_pages-1, or a token past pages_per_seq * page_size
+ * (past total_keys, packed), sets MISA_STATUS_BOUNDS and is skipped. */
+typedef struct {
+  void* k;
+  void* v;                       /* NULL: keys only (misa_cache_append) */
+  int32_t dtype;                 /* MISA_BF16 or MISA_FP16 */
+  int32_t num_kv_heads;          /* 1..256 */
+  int32_t head_dim;              /* 64 or 128 */
+  int32_t page_size;             /* tokens of a page, >= 1 */
+  int32_t num_pages;             /* pages behind k */
+  int32_t pages_per_seq;         /* entries of a sequence's row of page_table */
+  const int32_t* page_table;     /* device [S, page_table_stride], or NULL */
+  int64_t page_table_stride;
+  int64_t page_stride, token_stride, head_stride;  /* elements */
+} misa_kv_cache_t;
+
+/* What happens to a product before the softmax:
+ *     x = scale * (q . k[s]);   softcap > 0: x = softcap * tanh(x / softcap);
+ *     slopes != NULL: x -= slopes[head] * (q_pos[t] - s).
+ * An x of -inf counts as masked; a NaN reaches the row's output. */
+typedef struct {
+  float scale;
+  float softcap;                 /* 0: none */
+  const float* slopes;           /* device fp32 [num_q_heads], or NULL */
+} misa_attention_opts_t;
+
+/* Sequences that begin with the same tokens: those of group g are
+ * seq_offsets[g] .. seq_offsets[g+1]-1, and their first lens[g] tokens are
+ * read once for all of them, at the place where the group's first sequence
+ * keeps them (a length beyond that sequence's own, or beyond max_len, sets
+ * MISA_STATUS_BAD_INPUT and is cut).  A sequence in no group shares nothing. */
+typedef struct {
+  int32_t num_groups;            /* >= 0 */
+  int32_t max_len;               /* host-side upper bound on every length */
+  const int32_t* seq_offsets;    /* device [num_groups + 1], non-decreasing, within 0..S */
+  const int32_t* lens;           /* device [num_groups] */
+} misa_shared_prefix_t;
+
+/* Writes the keys and values of the problem's query tokens into the cache,
+ * with the rotation of their position applied on the way: token t of
+ * sequence s lands at token q_pos[t] of s.
+ *   k, v: [T, num_kv_heads, head_dim] of the cache's type, tokens
+ *   k_stride / v_stride elements apart (slices of a fused projection need no
+ *   copy), heads head_dim apart; v NULL exactly where cache->v is.
+ *   q: NULL, or [T, num_q_heads, head_dim], tokens q_stride apart; q_out
+ *   receives its rotated rows, contiguous.  q_out may be q itself where
+ *   q_stride = num_q_heads * head_dim; no other overlap is allowed.
+ *   rope: NULL (nothing is rotated), or fp32 [rope_rows, rope_dim], row p the
+ *   cosines of position p, then its sines, rope_dim / 2 each.  The first
+ *   rope_dim elements of a head are rotated, the rest copied; pair i is
+ *   elements (i, i + rope_dim / 2), or (2i, 2i + 1) with `interleaved`:
+ *       (x, y) -> (x cos - y sin, y cos + x sin)
+ *   in fp32, rounded once.  rope_dim: a multiple of 16, at most head_dim.
+ * A position outside its sequence sets MISA_STATUS_BAD_INPUT, one past
+ * rope_rows MISA_STATUS_BOUNDS; that token is left out, its q_out row too.
+ * Two tokens at one position of one sequence race for its row. */
+int misa_cache_append(const misa_problem_t* p, const misa_kv_cache_t* cache, const void* k,
+                      int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                      int64_t q_stride, int32_t num_q_heads, void* q_out, const float* rope,
+                      int32_t rope_rows, int32_t rope_dim, int32_t interleaved,
+                      misa_stream_t stream);
+
+/* Attention of every query over tokens 0..q_pos[t] of its sequence:
+ *     out[t,h] = sum_s softmax_s(x[t,h,s]) v[s, h / (num_q_heads / num_kv_heads)]
+ *   q, out [T, num_q_heads, head_dim] of the cache's type, contiguous;
+ *   num_q_heads a multiple of num_kv_heads, at most 64 times as many heads
+ *   per key head; lse: NULL, or fp32 [T, num_q_heads] receiving
+ *   ln sum_s exp(x).  A query that sees no token (a position outside its
+ *   sequence, flagged MISA_STATUS_BAD_INPUT; every x masked) gets a row of
+ *   zeros and an lse of -inf.
+ *   share: NULL, or the sequences' common prefixes.
+ *   ws: misa_attention_workspace_size(p, cache, num_q_heads, 0, share) bytes,
+ *   256-byte aligned; contents need not be kept or cleared.  Calls that may
+ *   run at the same time need workspaces of their own.
+ * Products and sums in fp32; the softmax weights enter the second product
+ * rounded to the cache's type, their sum does not.  The same inputs give the
+ * same bits. */
+int misa_attention(const misa_problem_t* p, const misa_kv_cache_t* cache, const void* q,
+                   int32_t num_q_heads, const misa_attention_opts_t* opts,
+                   const misa_shared_prefix_t* share, void* out, float* lse, void* ws,
+                   size_t ws_bytes, misa_stream_t stream);
+
+/* Attention of every query over the tokens that an indexer selected for it:
+ * as misa_attention, with s running over idx[t, 0..k-1] (misa_score_topk and
+ * its relatives write it) instead of the whole prefix.
+ *   idx [T, k] int32 token indices within the sequence, any order; entries
+ *   < 0 are padding; one past the query's position sets
+ *   MISA_STATUS_BAD_INPUT and is skipped; a token listed twice counts twice.
+ *   1 <= k <= 65536.  ws: misa_attention_workspace_size(p, cache,
+ *   num_q_heads, k, NULL) bytes. */
+int misa_attention_selected(const misa_problem_t* p, const misa_kv_cache_t* cache, const void* q,
+                            int32_t num_q_heads, const misa_attention_opts_t* opts,
+                            const int32_t* idx, int32_t k, void* out, float* lse, void* ws,
+                            size_t ws_bytes, misa_stream_t stream);
+
+/* Bytes of workspace of misa_attention (k = 0) or misa_attention_selected
+ * (k >= 1, share NULL).  Never 0 for valid arguments; 0 on invalid ones. */
+size_t misa_attention_workspace_size(const misa_problem_t* p, const misa_kv_cache_t* cache,
+                                     int32_t num_q_heads, int32_t k,
+                                     const misa_shared_prefix_t* share);
+
 /* Synchronises `stream`, returns the status word of the current device in
  * *device_status (may be NULL) and clears it.  Returns MISA_OK when the word
  * was zero, else the MISA_ERR_DEVICE_* code of its lowest set bit;

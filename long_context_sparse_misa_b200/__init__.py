@@ -23,6 +23,8 @@ __all__ = [
     "route", "pool_keys_from", "score_topk", "hier_rerank", "dsa_index_dense", "stream_status",
     "selftest_timeout", "route_static", "EXPORTED", "Indexer", "profile_enable", "profile_collect",
     "block_workspace_size", "block_score_topk",
+    "KVCache", "SharedPrefix", "rope_table", "cache_append", "attention", "attention_selected",
+    "attention_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmisa.so")
@@ -34,6 +36,8 @@ EXPORTED = (
     "misa_route_static", "misa_score_topk", "misa_hier_rerank", "dsa_index_dense", "misa_stream_status",
     "misa_selftest_timeout", "misa_profile_enable", "misa_profile_collect",
     "misa_last_error_string", "misa_block_workspace_size", "misa_block_score_topk",
+    "misa_cache_append", "misa_attention", "misa_attention_selected",
+    "misa_attention_workspace_size",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -54,7 +58,26 @@ class _Problem(ctypes.Structure):
     ]
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [
+        ("k", _c_p), ("v", _c_p), ("dtype", _c_i32), ("num_kv_heads", _c_i32),
+        ("head_dim", _c_i32), ("page_size", _c_i32), ("num_pages", _c_i32),
+        ("pages_per_seq", _c_i32), ("page_table", _c_p), ("page_table_stride", _c_i64),
+        ("page_stride", _c_i64), ("token_stride", _c_i64), ("head_stride", _c_i64),
+    ]
+
+
+class _AttentionOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", _c_p)]
+
+
+class _SharedPrefix(ctypes.Structure):
+    _fields_ = [("num_groups", _c_i32), ("max_len", _c_i32), ("seq_offsets", _c_p),
+                ("lens", _c_p)]
+
+
 _PP = ctypes.POINTER(_Problem)
+_PK, _PA, _PS = (ctypes.POINTER(t) for t in (_KVCache, _AttentionOpts, _SharedPrefix))
 _sig = {
     "misa_workspace_size": (_c_sz, [_PP, _c_i32, _c_i32, _c_i32]),
     "misa_block_offsets": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_p, _c_p]),
@@ -79,6 +102,13 @@ _sig = {
     "misa_block_workspace_size": (_c_sz, [_PP, _c_i32]),
     "misa_block_score_topk": (ctypes.c_int, [_PP, _c_p, _c_p, _c_i32, _c_p, _c_p, _c_i32, _c_i32,
                                              _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "misa_cache_append": (ctypes.c_int, [_PP, _PK, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64,
+                                         _c_i32, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_p]),
+    "misa_attention": (ctypes.c_int, [_PP, _PK, _c_p, _c_i32, _PA, _PS, _c_p, _c_p, _c_p, _c_sz,
+                                      _c_p]),
+    "misa_attention_selected": (ctypes.c_int, [_PP, _PK, _c_p, _c_i32, _PA, _c_p, _c_i32, _c_p,
+                                               _c_p, _c_p, _c_sz, _c_p]),
+    "misa_attention_workspace_size": (_c_sz, [_PP, _PK, _c_i32, _c_i32, _PS]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(lib, _name)
@@ -234,6 +264,220 @@ def block_score_topk(prob: Problem, q_r, w_r, m: int, K, Kbar, n_blocks: int, k:
                                      ws.numel(), _stream(stream)), "misa_block_score_topk")
 
 
+# ---------------------------------------------------------------- cache and attention
+def _need(ok: bool, where: str, what: str) -> None:
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _rows_of(t, where: str, name: str, heads, dim: int, dtype, device):
+    """Checks [T, heads, dim] rows whose tokens may be strided; returns (T, heads, token stride)."""
+    _need(t.dim() == 3 and t.shape[2] == dim and (heads is None or t.shape[1] == heads), where,
+          f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], got {tuple(t.shape)}")
+    _need(t.dtype == dtype and t.device == device, where,
+          f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    n, h, d = t.shape
+    _need(n == 0 or (t.stride(2) == 1 and (h == 1 or t.stride(1) == d)), where,
+          f"{name}: the heads of a token must be contiguous")
+    return n, h, (h * d if n <= 1 else t.stride(0))
+
+
+class KVCache:
+    """A key/value cache for cache_append, attention and attention_selected.
+
+    Paged: k and v [num_pages, page_size, heads, dim] views with the last axis
+    contiguous (a cache that keeps its heads before its tokens is passed as
+    ``x.transpose(1, 2)``), and page_table int32 [S, pages]: token p of
+    sequence s is row p % page_size of page page_table[s, p // page_size].
+    Packed (page_table None): k and v [total_keys, heads, dim], the tokens of
+    sequence s from key_offsets[s] on, as the indexer's K.  bf16 or fp16,
+    dim 64 or 128.  v None: a cache of keys only, which can be appended to.
+    The tensors stay the caller's: nothing is copied, and what is written to
+    the page table later counts.
+    """
+
+    def __init__(self, k, v=None, page_table=None):
+        import torch
+        where = "KVCache"
+        codes = {torch.bfloat16: 0, torch.float16: 1}
+        _need(k.is_cuda, where, "k must be a CUDA tensor")
+        _need(k.dtype in codes, where, f"dtype {k.dtype} unsupported (bfloat16 or float16)")
+        dims = 3 if page_table is None else 4
+        _need(k.dim() == dims, where, f"k must have {dims} dimensions, got {tuple(k.shape)}")
+        _need(k.stride(-1) == 1, where, "the last axis must be contiguous")
+        if v is not None:
+            _need(v.shape == k.shape and v.stride() == k.stride() and v.dtype == k.dtype
+                  and v.device == k.device, where,
+                  "v must have k's shape, strides, dtype and device")
+        self.k, self.v, self.page_table = k, v, page_table
+        c = self.c = _KVCache(k=k.data_ptr() or None, v=None if v is None else v.data_ptr() or None,
+                              dtype=codes[k.dtype], num_kv_heads=k.shape[-2], head_dim=k.shape[-1],
+                              head_stride=k.stride(-2), token_stride=k.stride(-3))
+        if page_table is not None:
+            t = page_table
+            _need(t.dtype == torch.int32 and t.dim() == 2 and t.device == k.device
+                  and (t.shape[1] <= 1 or t.stride(1) == 1), where,
+                  "page_table must be int32 [S, pages] on the cache's device, rows contiguous")
+            c.page_size, c.num_pages, c.page_stride = k.shape[1], k.shape[0], k.stride(0)
+            c.pages_per_seq = t.shape[1]
+            c.page_table = t.data_ptr()
+            c.page_table_stride = max(t.stride(0), t.shape[1])
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    def _fits(self, prob: "Problem", where: str) -> None:
+        _need(prob.q_pos.device == self.k.device, where,
+              f"the problem is on {prob.q_pos.device}, the cache on {self.k.device}")
+        if self.page_table is None:
+            _need(self.k.shape[0] >= prob.c.total_keys, where,
+                  f"a packed cache of {self.k.shape[0]} rows for {prob.c.total_keys} keys")
+        else:
+            _need(self.page_table.shape[0] >= prob.c.num_seqs, where,
+                  f"a page table of {self.page_table.shape[0]} rows for {prob.c.num_seqs} sequences")
+
+
+class SharedPrefix:
+    """Sequences that begin with the same tokens: group g is sequences
+    seq_offsets[g] .. seq_offsets[g+1]-1, which share their first lens[g]
+    tokens.  attention reads those once, where the group's first sequence
+    keeps them.  max_len bounds every length that will be written to
+    ``lens`` later (default: the largest one now)."""
+
+    def __init__(self, seq_offsets, lens, device="cuda", max_len=None):
+        import numpy as np
+        import torch
+        so, n = np.asarray(seq_offsets, np.int32), np.asarray(lens, np.int32)
+        _need(so.ndim == 1 and n.ndim == 1 and len(so) == len(n) + 1
+              and bool((np.diff(so) >= 0).all()) and so[0] >= 0 and bool((n >= 0).all()),
+              "SharedPrefix", "needs non-decreasing seq_offsets [groups + 1] and lens [groups] >= 0")
+        self.max_len = int(n.max(initial=0)) if max_len is None else int(max_len)
+        self.last = int(so[-1])
+        self.seq_offsets = torch.from_numpy(so).to(device)
+        self.lens = torch.from_numpy(n).to(device)
+        self.c = _SharedPrefix(num_groups=len(n), max_len=self.max_len,
+                               seq_offsets=self.seq_offsets.data_ptr(),
+                               lens=self.lens.data_ptr() if len(n) else None)
+
+
+def _share_ref(share, prob, where):
+    if share is None:
+        return None
+    _need(share.last <= prob.c.num_seqs, where,
+          f"shared prefixes of {share.last} sequences in a batch of {prob.c.num_seqs}")
+    _need(share.seq_offsets.device == prob.q_pos.device, where,
+          "the shared prefixes are on another device than the problem")
+    return ctypes.byref(share.c)
+
+
+def rope_table(rows: int, dim: int, theta: float = 10000.0, device="cuda"):
+    """fp32 [rows, dim] for cache_append: cosines, then sines, of position *
+    theta^(-2i/dim); angles in fp64, so that far positions keep theirs."""
+    import torch
+    f = theta ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+def cache_append(prob: Problem, cache: KVCache, k, v=None, q=None, q_out=None, rope=None,
+                 interleaved: bool = False, stream=None) -> None:
+    """Write the problem's query tokens' keys and values into the cache, the
+    keys (and q, into q_out) rotated by their positions' rows of ``rope``."""
+    import torch
+    w = "cache_append"
+    cache._fits(prob, w)
+    dev, dt, d = cache.k.device, cache.k.dtype, cache.c.head_dim
+    T = prob.T
+    _need((v is None) == (cache.v is None), w, "v must be given exactly where the cache has values")
+    n, _, ks = _rows_of(k, w, "k", cache.c.num_kv_heads, d, dt, dev)
+    vs = 0
+    if v is not None:
+        nv, _, vs = _rows_of(v, w, "v", cache.c.num_kv_heads, d, dt, dev)
+        _need(nv == T, w, f"v has {nv} rows for {T} tokens")
+    _need(n == T, w, f"k has {n} rows for {T} tokens")
+    hq = qs = 0
+    _need((q is None) == (q_out is None), w, "q and q_out go together")
+    if q is not None:
+        nq, hq, qs = _rows_of(q, w, "q", None, d, dt, dev)
+        _need(nq == T, w, f"q has {nq} rows for {T} tokens")
+        _need(q_out.shape == q.shape and q_out.dtype == dt and q_out.device == dev
+              and q_out.is_contiguous(), w, "q_out must be contiguous, of q's shape, dtype and device")
+    rows = rd = 0
+    if rope is not None:
+        _need(rope.dim() == 2 and rope.dtype == torch.float32 and rope.device == dev
+              and rope.is_contiguous(), w, "rope must be contiguous fp32 [rows, dim] on the cache's device")
+        rows, rd = rope.shape
+    with torch.cuda.device(dev):
+        _check(lib.misa_cache_append(prob.ref, cache.ref, _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, hq,
+                                     _ptr(q_out), _ptr(rope), rows, rd, int(interleaved),
+                                     _stream(stream)), "misa_cache_append")
+
+
+def attention_workspace_size(prob: Problem, cache: KVCache, num_q_heads: int, k: int = 0,
+                             share: SharedPrefix = None) -> int:
+    """Bytes of workspace of attention (k = 0) or attention_selected with lists of k."""
+    import torch
+    with torch.cuda.device(cache.k.device):
+        n = lib.misa_attention_workspace_size(prob.ref, cache.ref, num_q_heads, k,
+                                              _share_ref(share, prob, "attention_workspace_size"))
+    if n == 0:
+        raise MisaError(1, "misa_attention_workspace_size")
+    return int(n)
+
+
+def _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes):
+    import torch
+    cache._fits(prob, w)
+    _need(cache.v is not None, w, "the cache has no values")
+    dev, d = cache.k.device, cache.c.head_dim
+    T, hq, _ = _rows_of(q, w, "q", None, d, cache.k.dtype, dev)
+    _need(T == prob.T and q.is_contiguous(), w, f"q must be contiguous with {prob.T} rows")
+    _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev and out.is_contiguous(),
+          w, "out must be contiguous, of q's shape, dtype and device")
+    if lse is not None:
+        _need(lse.shape == (T, hq) and lse.dtype == torch.float32 and lse.device == dev
+              and lse.is_contiguous(), w, f"lse must be contiguous fp32 [{T}, {hq}]")
+    if slopes is not None:
+        _need(slopes.shape == (hq,) and slopes.dtype == torch.float32 and slopes.device == dev
+              and slopes.is_contiguous(), w, f"slopes must be contiguous fp32 [{hq}]")
+    _need(ws.device == dev and ws.is_contiguous(), w, "the workspace must be contiguous on the cache's device")
+    opts = _AttentionOpts(scale=d ** -0.5 if scale is None else scale, softcap=softcap,
+                          slopes=None if slopes is None else slopes.data_ptr())
+    return hq, ctypes.byref(opts), ws.numel() * ws.element_size()
+
+
+def attention(prob: Problem, cache: KVCache, q, out, ws, lse=None, scale=None, softcap: float = 0.0,
+              slopes=None, share: SharedPrefix = None, stream=None) -> None:
+    """Attention of every query over its whole prefix in the cache; a prefix
+    that sequences share (``share``) is read once for all of them.  scale
+    defaults to dim^-1/2; softcap caps scores by a tanh; slopes [heads]
+    subtract slope * distance."""
+    import torch
+    w = "attention"
+    hq, opts, nb = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
+    with torch.cuda.device(cache.k.device):
+        _check(lib.misa_attention(prob.ref, cache.ref, _ptr(q), hq, opts, _share_ref(share, prob, w),
+                                  _ptr(out), _ptr(lse), _ptr(ws), nb, _stream(stream)),
+               "misa_attention")
+
+
+def attention_selected(prob: Problem, cache: KVCache, q, idx, out, ws, lse=None, scale=None,
+                       softcap: float = 0.0, slopes=None, stream=None) -> None:
+    """Attention of every query over the tokens idx [T, k] that an indexer
+    selected for it (entries < 0 are padding)."""
+    import torch
+    w = "attention_selected"
+    hq, opts, nb = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
+    _need(idx.dim() == 2 and idx.shape[0] == prob.T and idx.dtype == torch.int32
+          and idx.device == cache.k.device and idx.is_contiguous(), w,
+          f"idx must be contiguous int32 [{prob.T}, k] on the cache's device")
+    with torch.cuda.device(cache.k.device):
+        _check(lib.misa_attention_selected(prob.ref, cache.ref, _ptr(q), hq, opts, _ptr(idx),
+                                           idx.shape[1], _ptr(out), _ptr(lse), _ptr(ws), nb,
+                                           _stream(stream)), "misa_attention_selected")
+
+
 def stream_status(stream=None) -> int:
     """Synchronise the stream; return (code, status bits) and clear the status word."""
     st = _c_i32(0)
@@ -275,6 +519,7 @@ class Indexer:
               needs n_blocks at construction)
     All inputs are device tensors: K uint16/bf16 [total_keys, 128],
     q [T, H, 128] bf16 bits, w [T, H] float32.
+    attend(): attention over the tokens that the last of these selected.
     """
 
     def __init__(self, prob: Problem, m: int, k: int, k_cand: int = 0, device="cuda",
@@ -296,6 +541,7 @@ class Indexer:
         if k_cand:
             self.cand = torch.empty((T, k_cand), dtype=torch.int32, device=dev)
             self.cand_val = torch.empty((T, k_cand), dtype=torch.float32, device=dev)
+        self._attend = {}
         self.n_blocks = n_blocks
         if n_blocks:
             self.block_ws = torch.empty(block_workspace_size(prob, n_blocks), dtype=torch.uint8,
@@ -336,3 +582,21 @@ class Indexer:
         dsa_index_dense(self.prob, q, w, K, self.k, self.idx, self.val, self.ws, scores_dbg,
                         stream)
         return self.idx, self.val
+
+    def attend(self, q, cache: KVCache, out=None, lse=None, scale=None, softcap: float = 0.0,
+               slopes=None, stream=None):
+        """Attention of q [T, heads, dim] over the tokens of the last selection
+        (idx) in the key/value cache; returns out (a buffer of this object,
+        written anew by the next call, unless one is given)."""
+        import torch
+        size = attention_workspace_size(self.prob, cache, q.shape[1], self.k)
+        # kept per shape for this object's life: a captured step finds its addresses again
+        key = (tuple(q.shape), q.dtype, size)
+        if key not in self._attend:
+            self._attend[key] = (torch.empty(size, dtype=torch.uint8, device=q.device),
+                                 torch.empty(q.shape, dtype=q.dtype, device=q.device))
+        ws, own = self._attend[key]
+        out = own if out is None else out
+        attention_selected(self.prob, cache, q, self.idx, out, ws, lse, scale, softcap,
+                           slopes, stream)
+        return out

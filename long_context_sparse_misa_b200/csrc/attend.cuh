@@ -1,0 +1,207 @@
+// What the attention kernels share: their arguments, the division of a batch
+// into work items, the change of a product into a softmax exponent, and how
+// partial results are kept.
+#pragma once
+
+#include "cache.cuh"
+
+namespace misa {
+
+// Which keys a launch covers.
+enum AttendMode { kOwn = 0, kShared = 1, kSelected = 2 };
+
+struct AttendArgs {
+  CacheView c;
+  const uint16_t* q;   // [T, Hq, D]
+  uint16_t* out;       // [T, Hq, D]
+  float* lse;          // [T, Hq] or nullptr
+  const int32_t* qo;   // [S + 1]
+  const int32_t* q_pos;
+  const int32_t* idx;  // [T, k], selected mode
+  const int32_t* so;   // [ng + 1] shared prefixes (ng == 0: none)
+  const int32_t* slen; // [ng]
+  const float* slopes; // [Hq] or nullptr
+  float* part_o;       // [T * Hq, nslots, D]; nullptr: one launch writes the results
+  float* part_lse;     // [T * Hq, nslots], base 2
+  uint32_t* status;
+  float scale2;        // no cap: scale * log2(e); cap: 2 * scale / cap * log2(e)
+  float cap2;          // cap * log2(e), or 0
+  int S, T, Hq, Hkv, G, k, ng, max_shared, max_seq_len;
+  int chunk, nch_max;  // keys of an item; most items along the keys
+  int slot0, nslots;   // this launch's first slot of a row's partial results; slots of a row
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Product -> exponent of 2, without the bias.  cap tanh(u) is formed as
+// cap - 2 cap / (e^{2u} + 1): exact at both ends (e^{2u} = inf and 0), and off
+// by a rounding of the cap near zero, where tanh.approx would be off by 2^-11.
+template <bool PLAIN>
+__device__ __forceinline__ float exponent(float s, const AttendArgs& a) {
+  if (!PLAIN && a.cap2 > 0.f) return fmaf(-2.f * a.cap2, rcp(ex2(s * a.scale2) + 1.f), a.cap2);
+  return s * a.scale2;
+}
+
+// Tokens of sequence s, at most what the launch was sized for.
+__device__ __forceinline__ int seq_len(const AttendArgs& a, int s) {
+  const int64_t len = __ldg(a.c.ko + s + 1) - __ldg(a.c.ko + s);
+  return len < 0 ? 0 : (int)(len < a.max_seq_len ? len : a.max_seq_len);
+}
+
+// Shared tokens of group g, cut to what its first sequence has and to max_shared.
+__device__ __forceinline__ int shared_len(const AttendArgs& a, int g) {
+  const int s0 = __ldg(a.so + g);
+  if (s0 < 0 || s0 >= a.S) return 0;
+  return max(0, min(__ldg(a.slen + g), min(a.max_shared, seq_len(a, s0))));
+}
+
+// The group of sequence s, or -1.
+__device__ __forceinline__ int group_of(const AttendArgs& a, int s) {
+  if (a.ng == 0 || s < __ldg(a.so) || s >= __ldg(a.so + a.ng)) return -1;
+  return upper_segment<int32_t>(a.so, a.ng, s);
+}
+
+__device__ __forceinline__ int prefix_of(const AttendArgs& a, int s) {
+  const int g = group_of(a, s);
+  return g < 0 ? 0 : shared_len(a, g);
+}
+
+// Items along the keys: own mode at least one (a row that sees nothing is
+// written by it), shared mode none for an empty prefix.
+__device__ __forceinline__ int own_chunks(const AttendArgs& a, int s, int chunk, int nch_max) {
+  const int own = seq_len(a, s) - prefix_of(a, s);
+  return min(nch_max, max(1, (max(own, 0) + chunk - 1) / chunk));
+}
+__device__ __forceinline__ int shared_chunks(const AttendArgs& a, int g, int chunk, int nch_max) {
+  return min(nch_max, (shared_len(a, g) + chunk - 1) / chunk);
+}
+
+// Query rows of group g (its sequences' queries are consecutive).
+__device__ __forceinline__ int2 group_queries(const AttendArgs& a, int g) {
+  const int lo = max(0, min(__ldg(a.so + g), a.S)), hi = max(lo, min(__ldg(a.so + g + 1), a.S));
+  return make_int2(__ldg(a.qo + lo), __ldg(a.qo + hi));
+}
+
+// One work item: rows r0 .. r0+nrows-1 of one key head, row r being query
+// qb + r / G, head h * G + r % G; keys [k0, k1) of sequence seq (in selected
+// mode: entries [k0, k1) of the query's list).
+struct Item {
+  int seq, qb, r0, nrows, h, k0, k1, slot;
+};
+
+// The items of own and shared mode run over units (sequences or groups), in
+// each over row tiles of `rows`, in each over the chunks of its keys, and
+// innermost over the key heads.  Their count per unit follows from device
+// data, so that every block adds it up for itself: thread i for the i-th
+// stretch of units, then a scan.  sums[i] is the count before stretch i,
+// sums[n] (returned) all of them.
+template <int MODE>
+__device__ __forceinline__ int unit_items(const AttendArgs& a, int u, int rows) {
+  const int2 q = MODE == kOwn ? make_int2(__ldg(a.qo + u), __ldg(a.qo + u + 1)) : group_queries(a, u);
+  const int tiles = (int)(((int64_t)max(0, min(q.y, a.T) - q.x) * a.G + rows - 1) / rows);
+  return tiles == 0 ? 0
+         : tiles * (MODE == kOwn ? own_chunks(a, u, a.chunk, a.nch_max)
+                                 : shared_chunks(a, u, a.chunk, a.nch_max));
+}
+
+template <int MODE, int THREADS>
+__device__ __forceinline__ int count_items(const AttendArgs& a, int rows, int* sums) {
+  const int units = MODE == kOwn ? a.S : a.ng;
+  const int per = (units + THREADS - 1) / THREADS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n = 0;
+  for (int u = threadIdx.x * per; u < min(units, ((int)threadIdx.x + 1) * per); ++u)
+    n += unit_items<MODE>(a, u, rows);
+  int x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[THREADS + 1 + warp] = x;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += sums[THREADS + 1 + w];
+  sums[threadIdx.x] = before + x - n;
+  if (threadIdx.x == THREADS - 1) sums[THREADS] = before + x;
+  __syncthreads();
+  return sums[THREADS];
+}
+
+// Item `i` (without the head) of those that count_items counted; every thread
+// finds the same one.
+template <int MODE, int THREADS>
+__device__ __forceinline__ void find_item(const AttendArgs& a, int rows, const int* sums, int i, Item& it) {
+  const int units = MODE == kOwn ? a.S : a.ng;
+  const int per = (units + THREADS - 1) / THREADS;
+  int u = upper_segment<int>(sums, THREADS, i) * per;
+  i -= sums[u / per];
+  for (;; ++u) {
+    const int n = unit_items<MODE>(a, u, rows);
+    if (i < n || u + 1 >= units) break;
+    i -= n;
+  }
+  const int2 q = MODE == kOwn ? make_int2(__ldg(a.qo + u), __ldg(a.qo + u + 1)) : group_queries(a, u);
+  const int nch = MODE == kOwn ? own_chunks(a, u, a.chunk, a.nch_max)
+                               : shared_chunks(a, u, a.chunk, a.nch_max);
+  const int all = max(0, min(q.y, a.T) - q.x) * a.G;
+  const int tiles = (all + rows - 1) / rows;
+  // the last row tiles see the most keys: they start first
+  const int tile = tiles - 1 - i / nch, c = i % nch;
+  it.qb = q.x;
+  it.r0 = tile * rows;
+  it.nrows = min(rows, all - it.r0);
+  it.slot = a.slot0 + c;
+  const int lo = MODE == kOwn ? prefix_of(a, u) : 0;
+  const int hi = MODE == kOwn ? seq_len(a, u) : shared_len(a, u);
+  it.seq = MODE == kOwn ? u : __ldg(a.so + u);
+  it.k0 = min(hi, lo + c * a.chunk);
+  it.k1 = c == nch - 1 ? hi : min(hi, lo + (c + 1) * a.chunk);
+}
+
+// Selected mode: items run over the queries, their row tiles, the chunks of
+// their lists, and innermost over the key heads.  False: a padding row.
+__device__ __forceinline__ bool find_selected(const AttendArgs& a, int rows, int i, Item& it) {
+  const int tiles = (a.G + rows - 1) / rows;
+  const int c = i % a.nch_max;
+  i /= a.nch_max;
+  const int tile = i % tiles;
+  it.qb = i / tiles;
+  it.r0 = tile * rows;
+  it.nrows = min(rows, a.G - it.r0);
+  it.slot = a.slot0 + c;
+  it.k0 = c * a.chunk;
+  it.k1 = min(a.k, it.k0 + a.chunk);
+  if (it.qb >= __ldg(a.qo + a.S)) return false;
+  it.seq = warp_segment(a.qo, a.S, it.qb);
+  return true;
+}
+
+// Position of query t, or -1 (flagged) where it is outside its sequence.
+__device__ __forceinline__ int checked_pos(const AttendArgs& a, int t, int seq) {
+  const int pos = __ldg(a.q_pos + t);
+  if (pos < 0 || pos >= seq_len(a, seq)) {
+    set_status(a.status, MISA_STATUS_BAD_INPUT);
+    return -1;
+  }
+  return pos;
+}
+
+}  // namespace misa
