@@ -265,21 +265,36 @@ def block_score_topk(prob: Problem, q_r, w_r, m: int, K, Kbar, n_blocks: int, k:
 
 
 # ---------------------------------------------------------------- cache and attention
-def _need(ok: bool, where: str, what: str) -> None:
-    if not ok:
-        raise ValueError(f"{where}: {what}")
+# These run once per layer and step, on calls of a few microseconds of GPU
+# time: a check costs an attribute or two, and only a refusal builds its text.
+def _refuse(where: str, what: str):
+    raise ValueError(f"{where}: {what}")
 
 
-def _rows_of(t, where: str, name: str, heads, dim: int, dtype, device):
-    """Checks [T, heads, dim] rows whose tokens may be strided; returns (T, heads, token stride)."""
-    _need(t.dim() == 3 and t.shape[2] == dim and (heads is None or t.shape[1] == heads), where,
-          f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], got {tuple(t.shape)}")
-    _need(t.dtype == dtype and t.device == device, where,
-          f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    n, h, d = t.shape
-    _need(n == 0 or (t.stride(2) == 1 and (h == 1 or t.stride(1) == d)), where,
-          f"{name}: the heads of a token must be contiguous")
-    return n, h, (h * d if n <= 1 else t.stride(0))
+def _token_stride(t, where: str, name: str, heads: int, dim: int, like) -> int:
+    """Elements between the tokens of t, which must be [T, heads, dim] of like's dtype and
+    device, the heads of a token contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        _refuse(where, f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        _refuse(where, f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    step = t.stride()
+    if shape[0] and (step[2] != 1 or (heads > 1 and step[1] != dim)):
+        _refuse(where, f"{name}: the heads of a token must be contiguous, got strides {step}")
+    return heads * dim if shape[0] <= 1 else step[0]
+
+
+def _on(cache, call, *args, stream):
+    """call(*args, stream) with the cache's device current."""
+    import torch
+    index = cache.device.index
+    if torch.cuda.current_device() == index:
+        s = torch.cuda.current_stream() if stream is None else stream
+        return call(*args, s.cuda_stream)
+    with torch.cuda.device(index):
+        s = torch.cuda.current_stream() if stream is None else stream
+        return call(*args, s.cuda_stream)
 
 
 class KVCache:
@@ -298,44 +313,44 @@ class KVCache:
 
     def __init__(self, k, v=None, page_table=None):
         import torch
-        where = "KVCache"
+        w = "KVCache"
         codes = {torch.bfloat16: 0, torch.float16: 1}
-        _need(k.is_cuda, where, "k must be a CUDA tensor")
-        _need(k.dtype in codes, where, f"dtype {k.dtype} unsupported (bfloat16 or float16)")
+        if not k.is_cuda:
+            _refuse(w, "k must be a CUDA tensor")
+        if k.dtype not in codes:
+            _refuse(w, f"dtype {k.dtype} unsupported (bfloat16 or float16)")
         dims = 3 if page_table is None else 4
-        _need(k.dim() == dims, where, f"k must have {dims} dimensions, got {tuple(k.shape)}")
-        _need(k.stride(-1) == 1, where, "the last axis must be contiguous")
-        if v is not None:
-            _need(v.shape == k.shape and v.stride() == k.stride() and v.dtype == k.dtype
-                  and v.device == k.device, where,
-                  "v must have k's shape, strides, dtype and device")
+        if k.dim() != dims or k.stride(-1) != 1:
+            _refuse(w, f"k must have {dims} dimensions, the last contiguous, got {tuple(k.shape)}")
+        if v is not None and (v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype
+                              or v.device != k.device):
+            _refuse(w, "v must have k's shape, strides, dtype and device")
         self.k, self.v, self.page_table = k, v, page_table
+        self.device, self.dtype, self.heads, self.dim = k.device, k.dtype, k.shape[-2], k.shape[-1]
         c = self.c = _KVCache(k=k.data_ptr() or None, v=None if v is None else v.data_ptr() or None,
-                              dtype=codes[k.dtype], num_kv_heads=k.shape[-2], head_dim=k.shape[-1],
+                              dtype=codes[k.dtype], num_kv_heads=self.heads, head_dim=self.dim,
                               head_stride=k.stride(-2), token_stride=k.stride(-3))
+        self.seqs = None  # packed: bounded by the rows instead
         if page_table is not None:
             t = page_table
-            _need(t.dtype == torch.int32 and t.dim() == 2 and t.device == k.device
-                  and (t.shape[1] <= 1 or t.stride(1) == 1), where,
-                  "page_table must be int32 [S, pages] on the cache's device, rows contiguous")
+            if (t.dtype != torch.int32 or t.dim() != 2 or t.device != k.device
+                    or (t.shape[1] > 1 and t.stride(1) != 1)):
+                _refuse(w, "page_table must be int32 [S, pages] on the cache's device, rows contiguous")
+            self.seqs = t.shape[0]
             c.page_size, c.num_pages, c.page_stride = k.shape[1], k.shape[0], k.stride(0)
             c.pages_per_seq = t.shape[1]
             c.page_table = t.data_ptr()
             c.page_table_stride = max(t.stride(0), t.shape[1])
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
+        self.ref = ctypes.byref(c)
 
     def _fits(self, prob: "Problem", where: str) -> None:
-        _need(prob.q_pos.device == self.k.device, where,
-              f"the problem is on {prob.q_pos.device}, the cache on {self.k.device}")
-        if self.page_table is None:
-            _need(self.k.shape[0] >= prob.c.total_keys, where,
-                  f"a packed cache of {self.k.shape[0]} rows for {prob.c.total_keys} keys")
-        else:
-            _need(self.page_table.shape[0] >= prob.c.num_seqs, where,
-                  f"a page table of {self.page_table.shape[0]} rows for {prob.c.num_seqs} sequences")
+        if prob.q_pos.device != self.device:
+            _refuse(where, f"the problem is on {prob.q_pos.device}, the cache on {self.device}")
+        if self.seqs is None:
+            if self.k.shape[0] < prob.c.total_keys:
+                _refuse(where, f"a packed cache of {self.k.shape[0]} rows for {prob.c.total_keys} keys")
+        elif self.seqs < prob.c.num_seqs:
+            _refuse(where, f"a page table of {self.seqs} rows for {prob.c.num_seqs} sequences")
 
 
 class SharedPrefix:
@@ -349,9 +364,10 @@ class SharedPrefix:
         import numpy as np
         import torch
         so, n = np.asarray(seq_offsets, np.int32), np.asarray(lens, np.int32)
-        _need(so.ndim == 1 and n.ndim == 1 and len(so) == len(n) + 1
-              and bool((np.diff(so) >= 0).all()) and so[0] >= 0 and bool((n >= 0).all()),
-              "SharedPrefix", "needs non-decreasing seq_offsets [groups + 1] and lens [groups] >= 0")
+        if (so.ndim != 1 or n.ndim != 1 or len(so) != len(n) + 1 or (np.diff(so) < 0).any()
+                or so[0] < 0 or (n < 0).any()):
+            _refuse("SharedPrefix",
+                    "needs non-decreasing seq_offsets [groups + 1] and lens [groups], all >= 0")
         self.max_len = int(n.max(initial=0)) if max_len is None else int(max_len)
         self.last = int(so[-1])
         self.seq_offsets = torch.from_numpy(so).to(device)
@@ -359,16 +375,17 @@ class SharedPrefix:
         self.c = _SharedPrefix(num_groups=len(n), max_len=self.max_len,
                                seq_offsets=self.seq_offsets.data_ptr(),
                                lens=self.lens.data_ptr() if len(n) else None)
+        self.ref = ctypes.byref(self.c)
 
 
 def _share_ref(share, prob, where):
     if share is None:
         return None
-    _need(share.last <= prob.c.num_seqs, where,
-          f"shared prefixes of {share.last} sequences in a batch of {prob.c.num_seqs}")
-    _need(share.seq_offsets.device == prob.q_pos.device, where,
-          "the shared prefixes are on another device than the problem")
-    return ctypes.byref(share.c)
+    if share.last > prob.c.num_seqs:
+        _refuse(where, f"shared prefixes of {share.last} sequences in a batch of {prob.c.num_seqs}")
+    if share.seq_offsets.device != prob.q_pos.device:
+        _refuse(where, "the shared prefixes are on another device than the problem")
+    return share.ref
 
 
 def rope_table(rows: int, dim: int, theta: float = 10000.0, device="cuda"):
@@ -387,38 +404,41 @@ def cache_append(prob: Problem, cache: KVCache, k, v=None, q=None, q_out=None, r
     import torch
     w = "cache_append"
     cache._fits(prob, w)
-    dev, dt, d = cache.k.device, cache.k.dtype, cache.c.head_dim
-    T = prob.T
-    _need((v is None) == (cache.v is None), w, "v must be given exactly where the cache has values")
-    n, _, ks = _rows_of(k, w, "k", cache.c.num_kv_heads, d, dt, dev)
-    vs = 0
+    like, d, heads, T = cache.k, cache.dim, cache.heads, prob.T
+    if (v is None) != (cache.v is None):
+        _refuse(w, "v must be given exactly where the cache has values")
+    if (q is None) != (q_out is None):
+        _refuse(w, "q and q_out go together")
+    ks = _token_stride(k, w, "k", heads, d, like)
+    vs = hq = qs = rows = turned = 0
     if v is not None:
-        nv, _, vs = _rows_of(v, w, "v", cache.c.num_kv_heads, d, dt, dev)
-        _need(nv == T, w, f"v has {nv} rows for {T} tokens")
-    _need(n == T, w, f"k has {n} rows for {T} tokens")
-    hq = qs = 0
-    _need((q is None) == (q_out is None), w, "q and q_out go together")
+        vs = _token_stride(v, w, "v", heads, d, like)
     if q is not None:
-        nq, hq, qs = _rows_of(q, w, "q", None, d, dt, dev)
-        _need(nq == T, w, f"q has {nq} rows for {T} tokens")
-        _need(q_out.shape == q.shape and q_out.dtype == dt and q_out.device == dev
-              and q_out.is_contiguous(), w, "q_out must be contiguous, of q's shape, dtype and device")
-    rows = rd = 0
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _token_stride(q, w, "q", hq, d, like)
+        if (q_out.shape != q.shape or q_out.dtype != like.dtype or q_out.device != like.device
+                or not q_out.is_contiguous()):
+            _refuse(w, "q_out must be contiguous, of q's shape, dtype and device")
+    if k.shape[0] != T or (v is not None and v.shape[0] != T) or (q is not None and q.shape[0] != T):
+        _refuse(w, f"k, v and q must have the problem's {T} rows")
     if rope is not None:
-        _need(rope.dim() == 2 and rope.dtype == torch.float32 and rope.device == dev
-              and rope.is_contiguous(), w, "rope must be contiguous fp32 [rows, dim] on the cache's device")
-        rows, rd = rope.shape
-    with torch.cuda.device(dev):
-        _check(lib.misa_cache_append(prob.ref, cache.ref, _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, hq,
-                                     _ptr(q_out), _ptr(rope), rows, rd, int(interleaved),
-                                     _stream(stream)), "misa_cache_append")
+        if (rope.dim() != 2 or rope.dtype != torch.float32 or rope.device != like.device
+                or not rope.is_contiguous()):
+            _refuse(w, "rope must be contiguous fp32 [rows, dim] on the cache's device")
+        rows, turned = rope.shape
+    code = _on(cache, lib.misa_cache_append, prob.ref, cache.ref, k.data_ptr(), ks,
+               None if v is None else v.data_ptr(), vs, None if q is None else q.data_ptr(), qs, hq,
+               None if q is None else q_out.data_ptr(), None if rope is None else rope.data_ptr(),
+               rows, turned, int(interleaved), stream=stream)
+    if code:
+        raise MisaError(code, "misa_cache_append")
 
 
 def attention_workspace_size(prob: Problem, cache: KVCache, num_q_heads: int, k: int = 0,
                              share: SharedPrefix = None) -> int:
     """Bytes of workspace of attention (k = 0) or attention_selected with lists of k."""
     import torch
-    with torch.cuda.device(cache.k.device):
+    with torch.cuda.device(cache.device):
         n = lib.misa_attention_workspace_size(prob.ref, cache.ref, num_q_heads, k,
                                               _share_ref(share, prob, "attention_workspace_size"))
     if n == 0:
@@ -429,22 +449,27 @@ def attention_workspace_size(prob: Problem, cache: KVCache, num_q_heads: int, k:
 def _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes):
     import torch
     cache._fits(prob, w)
-    _need(cache.v is not None, w, "the cache has no values")
-    dev, d = cache.k.device, cache.c.head_dim
-    T, hq, _ = _rows_of(q, w, "q", None, d, cache.k.dtype, dev)
-    _need(T == prob.T and q.is_contiguous(), w, f"q must be contiguous with {prob.T} rows")
-    _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev and out.is_contiguous(),
-          w, "out must be contiguous, of q's shape, dtype and device")
-    if lse is not None:
-        _need(lse.shape == (T, hq) and lse.dtype == torch.float32 and lse.device == dev
-              and lse.is_contiguous(), w, f"lse must be contiguous fp32 [{T}, {hq}]")
-    if slopes is not None:
-        _need(slopes.shape == (hq,) and slopes.dtype == torch.float32 and slopes.device == dev
-              and slopes.is_contiguous(), w, f"slopes must be contiguous fp32 [{hq}]")
-    _need(ws.device == dev and ws.is_contiguous(), w, "the workspace must be contiguous on the cache's device")
-    opts = _AttentionOpts(scale=d ** -0.5 if scale is None else scale, softcap=softcap,
-                          slopes=None if slopes is None else slopes.data_ptr())
-    return hq, ctypes.byref(opts), ws.numel() * ws.element_size()
+    if cache.v is None:
+        _refuse(w, "the cache has no values")
+    shape, dev = q.shape, cache.device
+    if len(shape) != 3 or shape[0] != prob.T or shape[2] != cache.dim or not q.is_contiguous():
+        _refuse(w, f"q must be contiguous [{prob.T}, heads, {cache.dim}], got {tuple(shape)}")
+    if q.dtype != cache.dtype or q.device != dev:
+        _refuse(w, f"q must be {cache.dtype} on {dev}, got {q.dtype} on {q.device}")
+    if out.shape != shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        _refuse(w, "out must be contiguous, of q's shape, dtype and device")
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or lse.device != dev
+                            or not lse.is_contiguous()):
+        _refuse(w, f"lse must be contiguous fp32 {tuple(shape[:2])}")
+    if slopes is not None and (slopes.shape != shape[1:2] or slopes.dtype != torch.float32
+                               or slopes.device != dev or not slopes.is_contiguous()):
+        _refuse(w, f"slopes must be contiguous fp32 [{shape[1]}]")
+    if ws.device != dev or not ws.is_contiguous():
+        _refuse(w, "the workspace must be contiguous on the cache's device")
+    opts = _AttentionOpts(cache.dim ** -0.5 if scale is None else scale, softcap,
+                          None if slopes is None else slopes.data_ptr())
+    return (shape[1], ctypes.byref(opts), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def attention(prob: Problem, cache: KVCache, q, out, ws, lse=None, scale=None, softcap: float = 0.0,
@@ -453,13 +478,12 @@ def attention(prob: Problem, cache: KVCache, q, out, ws, lse=None, scale=None, s
     that sequences share (``share``) is read once for all of them.  scale
     defaults to dim^-1/2; softcap caps scores by a tanh; slopes [heads]
     subtract slope * distance."""
-    import torch
     w = "attention"
-    hq, opts, nb = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
-    with torch.cuda.device(cache.k.device):
-        _check(lib.misa_attention(prob.ref, cache.ref, _ptr(q), hq, opts, _share_ref(share, prob, w),
-                                  _ptr(out), _ptr(lse), _ptr(ws), nb, _stream(stream)),
-               "misa_attention")
+    heads, opts, *rest = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
+    code = _on(cache, lib.misa_attention, prob.ref, cache.ref, q.data_ptr(), heads, opts,
+               _share_ref(share, prob, w), *rest, stream=stream)
+    if code:
+        raise MisaError(code, "misa_attention")
 
 
 def attention_selected(prob: Problem, cache: KVCache, q, idx, out, ws, lse=None, scale=None,
@@ -468,14 +492,14 @@ def attention_selected(prob: Problem, cache: KVCache, q, idx, out, ws, lse=None,
     selected for it (entries < 0 are padding)."""
     import torch
     w = "attention_selected"
-    hq, opts, nb = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
-    _need(idx.dim() == 2 and idx.shape[0] == prob.T and idx.dtype == torch.int32
-          and idx.device == cache.k.device and idx.is_contiguous(), w,
-          f"idx must be contiguous int32 [{prob.T}, k] on the cache's device")
-    with torch.cuda.device(cache.k.device):
-        _check(lib.misa_attention_selected(prob.ref, cache.ref, _ptr(q), hq, opts, _ptr(idx),
-                                           idx.shape[1], _ptr(out), _ptr(lse), _ptr(ws), nb,
-                                           _stream(stream)), "misa_attention_selected")
+    heads, opts, *rest = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
+    if (idx.dim() != 2 or idx.shape[0] != prob.T or idx.dtype != torch.int32
+            or idx.device != cache.device or not idx.is_contiguous()):
+        _refuse(w, f"idx must be contiguous int32 [{prob.T}, k] on the cache's device")
+    code = _on(cache, lib.misa_attention_selected, prob.ref, cache.ref, q.data_ptr(), heads, opts,
+               idx.data_ptr(), idx.shape[1], *rest, stream=stream)
+    if code:
+        raise MisaError(code, "misa_attention_selected")
 
 
 def stream_status(stream=None) -> int:

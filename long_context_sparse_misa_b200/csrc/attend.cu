@@ -26,6 +26,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
+constexpr int kTcRows = 48;  // rows of a unit from which the tcgen05 kernel is used
 
 template <int D, int WM, int KB>
 struct Shape {
@@ -40,7 +41,7 @@ struct Shape {
   static constexpr int big = ring > merge ? ring : merge;
   // q | ring (later the groups' partial rows) | key positions | stage flags | row positions | m, l | scan
   static constexpr int bytes = q_bytes + big + groups * kStages * KB * 4 + groups * kStages * 4 * WM + rows * 4 +
-                               groups * rows * 8 + (kThreads + 1 + kWarps) * 4 + 64;
+                               groups * rows * 8 + (kScan + 1 + kScan / 32) * 4 + 16 + 64;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -84,10 +85,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   uint8_t* s_q = smem;
   uint8_t* s_ring = s_q + Sh::q_bytes;
   int* s_key = reinterpret_cast<int*>(s_ring + Sh::big);
-  int* s_plain = s_key + Sh::groups * kStages * KB;
-  int* s_pos = s_plain + Sh::groups * kStages * WM;
+  int* s_mask = s_key + Sh::groups * kStages * KB;
+  int* s_pos = s_mask + Sh::groups * kStages * WM;
   float* s_ml = reinterpret_cast<float*>(s_pos + Sh::rows);
   int* s_sum = reinterpret_cast<int*>(s_ml + Sh::groups * Sh::rows * 2);
+
+  volatile int* s_cut = s_sum + kScan + 1 + kScan / 32;  // something was cut out of a value block
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wm = warp % WM, grp = warp / WM;
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   if constexpr (MODE == kSelected) {
     total = a.T * ((a.G + Sh::rows - 1) / Sh::rows) * a.nch_max;
   } else {
-    total = count_items<MODE, kThreads>(a, Sh::rows, s_sum);
+    total = count_items<MODE>(a, Sh::rows, s_sum);
   }
   for (int64_t w = blockIdx.x; w < (int64_t)total * a.Hkv; w += gridDim.x) {
     Item it;
@@ -105,10 +108,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     if constexpr (MODE == kSelected) {
       if (!find_selected(a, Sh::rows, (int)(w / a.Hkv), it)) continue;
     } else {
-      find_item<MODE, kThreads>(a, Sh::rows, s_sum, (int)(w / a.Hkv), it);
+      find_item<MODE>(a, Sh::rows, s_sum, (int)(w / a.Hkv), it);
     }
     __syncthreads();  // the previous item is done with shared memory
 
+    if (threadIdx.x == 0) *s_cut = 0;
     // Rows: their queries' positions (-1 sees nothing) and, swizzled, their q.
     for (int r = threadIdx.x; r < Sh::rows; r += kThreads) {
       int pos = -1;
@@ -131,14 +135,17 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       *reinterpret_cast<uint4*>(s_q + r * Sh::row_bytes + ((c ^ (r & 7)) << 4)) = x;
     }
     __syncthreads();
-    // Furthest and nearest position of the real rows.
-    int far = -1, near = 0x7fffffff;
+    // Furthest and nearest position of the real rows; least: of those that see anything.
+    int far = -1, near = 0x7fffffff, least = 0x7fffffff;
     for (int r = lane; r < it.nrows; r += 32) {
-      far = max(far, s_pos[r]);
-      near = min(near, s_pos[r]);
+      const int pos = s_pos[r];
+      far = max(far, pos);
+      near = min(near, pos);
+      if (pos >= 0) least = min(least, pos);
     }
     far = __reduce_max_sync(0xffffffffu, far);
     near = __reduce_min_sync(0xffffffffu, near);
+    least = __reduce_min_sync(0xffffffffu, least);
     const int k1 = MODE == kSelected ? it.k1 : min(it.k1, far + 1);
     const int nblk = k1 > it.k0 ? (k1 - it.k0 + KB - 1) / KB : 0;
     const int mine = nblk > grp ? (nblk - grp + Sh::groups - 1) / Sh::groups : 0;  // blocks of this group
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     };
     uint8_t* ring = s_ring + grp * kStages * Sh::stage;
     int* keys = s_key + grp * kStages * KB;
-    int* plain = s_plain + (grp * kStages) * WM;
+    int* masks = s_mask + (grp * kStages) * WM;
     auto load = [&](int i, int key, int64_t row) {
       const int st = i % kStages;
       uint8_t* dst = ring + st * Sh::stage;
@@ -197,9 +204,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
           cp_async_16(d + Sh::half, a.c.v + e, off >= 0);
         }
         if (wm == 0 && lane < KB) keys[st * KB + lane] = row < 0 ? -1 : key;
-        // no key of the block needs a mask
-        const bool all = __all_sync(0xffffffffu, lane >= KB || (row >= 0 && key <= near));
-        if (lane == 0) plain[st * WM + wm] = all;
+        // 1: a key of the block needs a mask; 2: some rows see it, others not
+        const bool mask = !__all_sync(0xffffffffu, lane >= KB || (row >= 0 && key <= near));
+        const bool part = MODE != kSelected && __any_sync(0xffffffffu, lane < KB && row >= 0 && key > least);
+        if (lane == 0) masks[st * WM + wm] = part ? 2 : mask;
       }
       cp_async_commit();
     };
@@ -253,7 +261,18 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
           mma16816(s[n + 1], fq[ks], b[2], b[3], tag);
         }
       }
-      const bool mask = !plain[st * WM + wm];
+      const int mask = masks[st * WM + wm];
+      if (MODE != kSelected && mask == 2) {
+        bool cut = false;
+        for (int i = wm * 32 + lane; i < KB * kChunks; i += WM * 32) {
+          const int r = i / kChunks, c = i % kChunks;
+          if (keys[st * KB + r] > least)
+            cut |= cut_infinite<E>(reinterpret_cast<uint4*>(ring + st * Sh::stage + Sh::half + r * Sh::row_bytes +
+                                                           ((c ^ (r & 7)) << 4)));
+        }
+        if (cut) *s_cut = 1;
+        group_sync<WM>(grp);
+      }
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -377,7 +396,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that saw nothing: zeros
       const float lse2 = l == 0.f ? -INFINITY : ref + lg2(l);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] *= inv;
+      for (int j = 0; j < 8; ++j) acc[j] = l == 0.f ? 0.f : acc[j] * inv;
+      if (MODE != kSelected && *s_cut && least < s_pos[r])
+        poison<E, 8>(a, it.seq, it.h, c * 8, max(it.k0, least + 1), min(k1 - 1, s_pos[r]), acc);
       const int gr = it.r0 + r;
       const int64_t row = (int64_t)(it.qb + gr / a.G) * a.Hq + it.h * a.G + gr % a.G;
       if (a.part_o) {
@@ -504,7 +525,8 @@ int launch_width(const AttendArgs& a, int rows, int64_t bound, cudaStream_t st) 
 }
 
 template <int MODE>
-int launch_attend(const AttendArgs& a, int dtype, int D, int rows, int64_t bound, cudaStream_t st) {
+int launch_attend(const AttendArgs& a, int dtype, int D, bool tc, int rows, int64_t bound, cudaStream_t st) {
+  if (tc) return launch_attend_tc(a, MODE, rows, dtype, D, bound, st);
   if (dtype == MISA_BF16)
     return D == 128 ? launch_width<__nv_bfloat16, 128, MODE>(a, rows, bound, st)
                     : launch_width<__nv_bfloat16, 64, MODE>(a, rows, bound, st);
@@ -528,6 +550,7 @@ int launch_combine(const CombineArgs& c, int dtype, int D, cudaStream_t st) {
 // How a call is divided: from host-side bounds alone, so that a captured call
 // stays right when the device's lengths change within them.
 struct Part {
+  bool tc = false;     // tcgen05 (attend_tc.cu)
   int rows = 16;       // rows of an item
   int chunk = 1;       // keys of an item
   int nch = 0;         // most items along the keys (0: no launch)
@@ -543,17 +566,33 @@ struct Plan {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr int kMinChunk = 128;
+// Rows of an item for units (sequences, groups, queries) of about `rows` rows.
+void pick_rows(Part& p, int64_t rows) {
+  p.tc = rows >= kTcRows;
+  if (p.tc) p.rows = rows > 128 ? 256 : 128;
+  else p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
 
-int row_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
-// Key chunks so that `units` row tiles (heads included) over about `keys` keys
-// each fill two waves of blocks, but no chunk is below kMinChunk keys.
+// Cuts the keys of `units` row tiles (heads included), about `keys` each and
+// at most max_keys, into the number of chunks that ends first: the items fill
+// the GPU's places in whole waves, and an item costs its keys and a fixed part.
 void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys) {
-  const int64_t want = std::max<int64_t>(1, (int64_t)num_sms() * 4 / std::max<int64_t>(1, units));
-  int64_t chunk = std::max<int64_t>(kMinChunk, (keys + want - 1) / want);
+  const int64_t places = num_sms() * (p.tc ? 1 : 2);
+  const int64_t fixed = p.tc ? 512 : 192, least = p.tc ? 256 : 128;
+  units = std::max<int64_t>(1, units);
+  keys = std::max<int64_t>(1, std::min(keys, max_keys));
+  const int64_t most = std::min<int64_t>((keys + least - 1) / least, 4 * places / units + 1);
+  int64_t best = 1, best_cost = INT64_MAX;
+  for (int64_t c = 1; c <= most; ++c) {
+    const int64_t waves = (units * c + places - 1) / places;
+    const int64_t cost = waves * ((keys + c - 1) / c + fixed) + (c > 1 ? fixed + 8 * c : 0);
+    if (cost < best_cost) {
+      best = c;
+      best_cost = cost;
+    }
+  }
+  int64_t chunk = best == 1 ? max_keys : (keys + best - 1) / best;
   chunk = (chunk + 31) / 32 * 32;
-  if (chunk >= max_keys || want == 1) chunk = (max_keys + 31) / 32 * 32;
   p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
   p.nch = (int)((max_keys + p.chunk - 1) / p.chunk);
 }
@@ -563,25 +602,25 @@ Plan make_plan(const misa_problem_t* p, const misa_kv_cache_t* c, int Hq, int k,
   Plan pl;
   const int G = Hq / c->num_kv_heads;
   const int64_t T = p->num_queries, S = p->num_seqs, H = c->num_kv_heads;
+  auto tiles = [](int64_t rows, int64_t per) { return (rows + per - 1) / per; };
   if (k > 0) {
-    pl.own.rows = row_tile(G);
-    const int64_t tiles = T * ((G + pl.own.rows - 1) / pl.own.rows);
-    split_keys(pl.own, tiles * H, k, k);
-    pl.own.bound = tiles * H * pl.own.nch;
+    pick_rows(pl.own, G);
+    const int64_t units = T * tiles(G, pl.own.rows) * H;
+    split_keys(pl.own, units, k, k);
+    pl.own.bound = units * pl.own.nch;
   } else {
     const int64_t ng = share ? share->num_groups : 0, longest = ng ? share->max_len : 0;
-    const int64_t per_seq = (T + S - 1) / S * G;
-    pl.own.rows = row_tile(per_seq);
-    const int64_t tiles = T * G / pl.own.rows + S;
+    const int64_t per_seq = tiles(T, S) * G;
+    pick_rows(pl.own, per_seq);
     // what the prefixes hold is not read per sequence
     const int64_t keys = std::max<int64_t>(p->total_keys - (S - ng) * longest, p->total_keys / 16) / S + 1;
-    split_keys(pl.own, tiles * H, keys, p->max_seq_len);
-    pl.own.bound = tiles * H * pl.own.nch;
+    split_keys(pl.own, S * tiles(per_seq, pl.own.rows) * H, keys, p->max_seq_len);
+    pl.own.bound = (T * G / pl.own.rows + S) * H * pl.own.nch;
     if (ng && longest > 0) {
-      pl.shared.rows = row_tile(T * G / ng);
-      const int64_t st = T * G / pl.shared.rows + ng;
-      split_keys(pl.shared, st * H, longest, longest);
-      pl.shared.bound = st * H * pl.shared.nch;
+      const int64_t per_group = tiles(T, ng) * G;
+      pick_rows(pl.shared, per_group);
+      split_keys(pl.shared, ng * tiles(per_group, pl.shared.rows) * H, longest, longest);
+      pl.shared.bound = (T * G / pl.shared.rows + ng) * H * pl.shared.nch;
     }
   }
   pl.nslots = pl.own.nch + pl.shared.nch;
@@ -677,13 +716,13 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
     b.chunk = pl.shared.chunk;
     b.nch_max = pl.shared.nch;
     b.slot0 = 0;
-    if ((rc = launch_attend<kShared>(b, c->dtype, c->head_dim, pl.shared.rows, pl.shared.bound, st))) return rc;
+    if ((rc = launch_attend<kShared>(b, c->dtype, c->head_dim, pl.shared.tc, pl.shared.rows, pl.shared.bound, st))) return rc;
   }
   a.chunk = pl.own.chunk;
   a.nch_max = pl.own.nch;
   a.slot0 = pl.shared.nch;
-  rc = k > 0 ? launch_attend<kSelected>(a, c->dtype, c->head_dim, pl.own.rows, pl.own.bound, st)
-             : launch_attend<kOwn>(a, c->dtype, c->head_dim, pl.own.rows, pl.own.bound, st);
+  rc = k > 0 ? launch_attend<kSelected>(a, c->dtype, c->head_dim, pl.own.tc, pl.own.rows, pl.own.bound, st)
+             : launch_attend<kOwn>(a, c->dtype, c->head_dim, pl.own.tc, pl.own.rows, pl.own.bound, st);
   if (rc || !pl.partial) return rc;
   CombineArgs ca;
   ca.a = a;

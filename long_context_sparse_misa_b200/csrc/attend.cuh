@@ -3,6 +3,8 @@
 // partial results are kept.
 #pragma once
 
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace misa {
@@ -121,37 +123,44 @@ __device__ __forceinline__ int unit_items(const AttendArgs& a, int u, int rows) 
                                  : shared_chunks(a, u, a.chunk, a.nch_max));
 }
 
-template <int MODE, int THREADS>
+// sums: kScan + 1 + kScan / 32 ints; every thread of the block (at least
+// kScan of them) calls this.
+constexpr int kScan = 128;
+
+template <int MODE>
 __device__ __forceinline__ int count_items(const AttendArgs& a, int rows, int* sums) {
   const int units = MODE == kOwn ? a.S : a.ng;
-  const int per = (units + THREADS - 1) / THREADS;
+  const int per = (units + kScan - 1) / kScan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int n = 0;
-  for (int u = threadIdx.x * per; u < min(units, ((int)threadIdx.x + 1) * per); ++u)
-    n += unit_items<MODE>(a, u, rows);
-  int x = n;
+  int n = 0, x = 0;
+  if (threadIdx.x < kScan) {
+    for (int u = threadIdx.x * per; u < min(units, ((int)threadIdx.x + 1) * per); ++u)
+      n += unit_items<MODE>(a, u, rows);
+    x = n;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[kScan + 1 + warp] = x;
   }
-  if (lane == 31) sums[THREADS + 1 + warp] = x;
   __syncthreads();
-  int before = 0;
-  for (int w = 0; w < warp; ++w) before += sums[THREADS + 1 + w];
-  sums[threadIdx.x] = before + x - n;
-  if (threadIdx.x == THREADS - 1) sums[THREADS] = before + x;
+  if (threadIdx.x < kScan) {
+    for (int w = 0; w < warp; ++w) x += sums[kScan + 1 + w];
+    sums[threadIdx.x] = x - n;
+    if (threadIdx.x == kScan - 1) sums[kScan] = x;
+  }
   __syncthreads();
-  return sums[THREADS];
+  return sums[kScan];
 }
 
 // Item `i` (without the head) of those that count_items counted; every thread
 // finds the same one.
-template <int MODE, int THREADS>
+template <int MODE>
 __device__ __forceinline__ void find_item(const AttendArgs& a, int rows, const int* sums, int i, Item& it) {
   const int units = MODE == kOwn ? a.S : a.ng;
-  const int per = (units + THREADS - 1) / THREADS;
-  int u = upper_segment<int>(sums, THREADS, i) * per;
+  const int per = (units + kScan - 1) / kScan;
+  int u = upper_segment<int>(sums, kScan, i) * per;
   i -= sums[u / per];
   for (;; ++u) {
     const int n = unit_items<MODE>(a, u, rows);
@@ -203,5 +212,42 @@ __device__ __forceinline__ int checked_pos(const AttendArgs& a, int t, int seq) 
   }
   return pos;
 }
+
+// Values that no row may take from a masked place.  A weight of 0 times an
+// infinity is a NaN, so of keys that only some rows of an item see (those
+// behind `near`, its nearest position) what is not finite is cut out of the
+// tile, and `poison` gives it back to the rows that do see the key.
+// Returns the word without its elements that are not finite.
+template <typename E>
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  constexpr uint32_t M = std::is_same<E, __half>::value ? 0x7c00u : 0x7f80u;
+  if ((w & M) == M) w &= 0xffff0000u;
+  if ((w & (M << 16)) == (M << 16)) w &= 0x0000ffffu;
+  return w;
+}
+template <typename E>
+__device__ __forceinline__ bool cut_infinite(uint4* p) {
+  const uint4 x = *p;
+  const uint4 y = make_uint4(finite2<E>(x.x), finite2<E>(x.y), finite2<E>(x.z), finite2<E>(x.w));
+  if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) return false;
+  *p = y;
+  return true;
+}
+// Adds to o what is not finite of dims [d0, d0 + N) of keys [k0, k1]; N % 8 == 0.
+template <typename E, int N>
+__device__ __noinline__ void poison(const AttendArgs& a, int seq, int h, int d0, int k0, int k1, float* o) {
+  for (int j = k0; j <= k1; ++j) {
+    const int64_t r = cache_row(a.c, seq, j);
+    if (r < 0) continue;
+    const uint16_t* v = a.c.v + r + h * a.c.head_stride + d0;
+    for (int d = 0; d < N; ++d) {
+      const float x = to_float(__ldg(v + d), E());
+      if (!(fabsf(x) < INFINITY)) o[d] += x;
+    }
+  }
+}
+
+// attend_tc.cu: items of 128 rows (split) or 256 (pair) on tcgen05.
+int launch_attend_tc(const AttendArgs& a, int mode, int rows, int dtype, int D, int64_t bound, cudaStream_t st);
 
 }  // namespace misa

@@ -177,6 +177,26 @@ def test_what_later_tokens_hold_reaches_no_earlier_query():
         assert out[late].isnan().all()
 
 
+@pytest.mark.parametrize("hq,n,dt", [(2, 3, BF), (16, 3, FP), (32, 2, BF), (4, 150, BF), (4, 150, FP), (48, 1, BF)])
+def test_an_infinite_value_reaches_the_queries_that_see_it(hq, n, dt):
+    b = Batch([400, 333], _last([400, 333], n), hq, 1, page=16, dtype=dt)
+    clean, lse = b.attention()
+    for s, L in enumerate(b.lens):
+        for p, d, bad in ((L - 1, 3, float("inf")), (L - 1, 77, float("nan")), (max(0, L - 2), 5, -float("inf"))):
+            b.v[int(b.table[s, p // 16]), p % 16, 0, d] = bad
+    out, lse2 = b.attention()
+    assert_status_ok()
+    assert torch.equal(lse, lse2)
+    for t in range(b.T):
+        ahead = b.lens[b.seq[t]] - 1 - b.pos[t]
+        want = clean[t].clone()
+        if ahead < 1:
+            want[:, 3], want[:, 77] = float("inf"), float("nan")
+        if ahead < 2:
+            want[:, 5] = -float("inf")
+        assert torch.equal(out[t].nan_to_num(nan=123.0), want.nan_to_num(nan=123.0)), t
+
+
 def test_same_bits_again_on_another_stream_and_in_a_graph():
     b = Batch([3000, 1200, 5], _last([3000, 1200, 5], 2), 16, 2, 128, 16, BF)
     out, lse, ws = b.buffers()
