@@ -3,6 +3,7 @@
 // score.cu and topk.cu; this file only validates and sequences them.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -14,6 +15,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "cache.cuh"
 #include "internal.h"
 
 __device__ uint32_t g_misa_status;  // per-device status word (MISA_STATUS_* bits)
@@ -73,7 +75,9 @@ int set_smem_limit(const void* kernel, int bytes) {
   return MISA_OK;
 }
 
-int make_kmajor_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows) {
+namespace {
+int encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+               const cuuint64_t* strides, int box_rows) {
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!g_encode) {
@@ -87,21 +91,46 @@ int make_kmajor_map(CUtensorMap* map, const void* base, int64_t rows, int box_ro
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
   }
-  if (rows <= 0) rows = 1;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD * 2)};
-  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = g_encode(map, type, rank, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
-    set_error("cuTensorMapEncodeTiled failed (%d) rows=%lld box=%d", (int)r, (long long)rows,
-              box_rows);
+    set_error("cuTensorMapEncodeTiled failed (%d) rows=%lld box=%d", (int)r, (long long)dims[1], box_rows);
     return MISA_ERR_CUDA;
   }
   return MISA_OK;
+}
+int encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int dim, int64_t stride,
+                int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride * 2)};
+  return encode_map(map, type, base, 2, dims, strides, box_rows);
+}
+CUtensorMapDataType map_type(bool fp16) {
+  return fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+}  // namespace
+
+int make_kmajor_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows) {
+  return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, kD, kD, box_rows);
+}
+
+int make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim, int64_t stride, bool fp16) {
+  return encode_rows(map, map_type(fp16), base, rows, dim, stride, 1);
+}
+
+int make_box_map(CUtensorMap* map, const void* base, const CacheView& c, int heads, int dim, int box, bool fp16) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim),
+                              static_cast<cuuint64_t>(c.table ? c.page_size : std::max<int64_t>(1, c.total_keys)),
+                              static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(c.table ? std::max(1, c.num_pages) : 1)};
+  // a stride that nothing is multiplied by may be anything; the map wants a positive one
+  auto bytes = [&](int64_t elements, cuuint64_t n) { return static_cast<cuuint64_t>(n > 1 ? elements * 2 : dim * 2); };
+  const cuuint64_t strides[3] = {bytes(c.token_stride, dims[1]), bytes(c.head_stride, dims[2]),
+                                 bytes(c.page_stride, dims[3])};
+  return encode_map(map, map_type(fp16), base, 4, dims, strides, box);
 }
 
 namespace {

@@ -1,7 +1,7 @@
 // Attention over the key/value cache for few rows per key head (decode), by
 // warp-level matrix instructions, and the joining of partial results.
 //
-//     x = exponent(q . k) - slope (pos_q - pos_k),  out = sum 2^(x - m) v / sum 2^(x - m)
+//     x = change(q . k) - slope (pos_q - pos_k),  out = sum 2^(x - m) v / sum 2^(x - m)
 // in one pass over the keys with the running maximum m and sum of each row.
 //
 // A block of four warps takes 16 WM rows of one key head against one chunk of
@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <numeric>
 
 namespace misa {
 
@@ -74,8 +75,8 @@ __device__ __forceinline__ void group_sync(int group) {
   }
 }
 
-// MODE: which keys; PLAIN: neither cap nor bias (else both are looked at).
-template <typename E, int D, int WM, int KB, int MODE, bool PLAIN>
+// MODE: which keys; KIND: what is done to the products (Change).
+template <typename E, int D, int WM, int KB, int MODE, int KIND>
 __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
   pdl_wait_then_release();
   using Sh = Shape<D, WM, KB>;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     const int row0 = wm * 16 + (lane >> 2), row1 = row0 + 8;
     const int pos0 = s_pos[row0], pos1 = s_pos[row1];
     float sl0 = 0.f, sl1 = 0.f;
-    const bool bias = !PLAIN && a.slopes;
+    const bool bias = KIND == kBiased || (KIND == kCapped && a.slopes);
     if (bias) {
       sl0 = row0 < it.nrows ? __ldg(a.slopes + it.h * a.G + (it.r0 + row0) % a.G) * kLog2e : 0.f;
       sl1 = row1 < it.nrows ? __ldg(a.slopes + it.h * a.G + (it.r0 + row1) % a.G) * kLog2e : 0.f;
@@ -275,8 +276,19 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       }
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
+        if constexpr (KIND == kCapped) {
+          if (mask) {
+            const int2 kp = *reinterpret_cast<const int2*>(keys + st * KB + n * 8 + (lane & 3) * 2);
+            if (kp.x < 0 || kp.x > pos0) s[n][0] = 0.f;
+            if (kp.y < 0 || kp.y > pos0) s[n][1] = 0.f;
+            if (kp.x < 0 || kp.x > pos1) s[n][2] = 0.f;
+            if (kp.y < 0 || kp.y > pos1) s[n][3] = 0.f;
+          }
+          cap4(s[n][0], s[n][1], s[n][2], s[n][3], a);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = exponent<PLAIN>(s[n][j], a);
+          for (int j = 0; j < 4; ++j) s[n][j] *= a.scale2;
+        }
         if (bias || mask) {
           const int2 kp = *reinterpret_cast<const int2*>(keys + st * KB + n * 8 + (lane & 3) * 2);
           if (bias) {
@@ -496,10 +508,10 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
   if (threadIdx.x == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (ref + lg2(l)) * kLn2;
 }
 
-template <typename E, int D, int WM, int KB, int MODE, bool PLAIN>
+template <typename E, int D, int WM, int KB, int MODE, int KIND>
 int launch_rows(const AttendArgs& a, int64_t bound, cudaStream_t st) {
   using Sh = Shape<D, WM, KB>;
-  auto kern = attend_kernel<E, D, WM, KB, MODE, PLAIN>;
+  auto kern = attend_kernel<E, D, WM, KB, MODE, KIND>;
   int rc = set_smem_limit((const void*)kern, Sh::bytes);
   if (rc) return rc;
   // one wave of resident blocks walks the items
@@ -513,8 +525,9 @@ int launch_rows(const AttendArgs& a, int64_t bound, cudaStream_t st) {
 
 template <typename E, int D, int WM, int KB, int MODE>
 int launch_kind(const AttendArgs& a, int64_t bound, cudaStream_t st) {
-  return a.cap2 > 0.f || a.slopes ? launch_rows<E, D, WM, KB, MODE, false>(a, bound, st)
-                                  : launch_rows<E, D, WM, KB, MODE, true>(a, bound, st);
+  return a.cap2 > 0.f ? launch_rows<E, D, WM, KB, MODE, kCapped>(a, bound, st)
+         : a.slopes   ? launch_rows<E, D, WM, KB, MODE, kBiased>(a, bound, st)
+                      : launch_rows<E, D, WM, KB, MODE, kScaled>(a, bound, st);
 }
 
 template <typename E, int D, int MODE>
@@ -566,9 +579,34 @@ struct Plan {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The cache as rows of D elements a fixed step apart, which every stride is a
+// multiple of, so that a row has one index in a tensor map.  rows == 0: the
+// steps overlap, or there are more rows than an index holds.
+struct RowGrid {
+  int64_t unit = 0, rows = 0;
+};
+RowGrid row_grid(const misa_problem_t* p, const misa_kv_cache_t* c) {
+  const int64_t n[3] = {c->page_table ? c->num_pages : 1, c->page_table ? c->page_size : p->total_keys,
+                        c->num_kv_heads};
+  const int64_t step[3] = {c->page_stride, c->token_stride, c->head_stride};
+  RowGrid g;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1) g.unit = std::gcd(g.unit, step[i]);
+  if (g.unit == 0) g.unit = c->head_dim;
+  int64_t last = 0;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1) {
+      const int64_t s = step[i] / g.unit;
+      if (s && n[i] - 1 > (int64_t(1) << 31) / s) return RowGrid();
+      last += (n[i] - 1) * s;
+    }
+  if (g.unit >= c->head_dim && last < (int64_t(1) << 31) - 2 && g.unit < (int64_t(1) << 38)) g.rows = last + 1;
+  return g;
+}
+
 // Rows of an item for units (sequences, groups, queries) of about `rows` rows.
-void pick_rows(Part& p, int64_t rows) {
-  p.tc = rows >= kTcRows;
+void pick_rows(Part& p, int64_t rows, bool grid) {
+  p.tc = grid && rows >= kTcRows;
   if (p.tc) p.rows = rows > 128 ? 256 : 128;
   else p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
@@ -602,23 +640,24 @@ Plan make_plan(const misa_problem_t* p, const misa_kv_cache_t* c, int Hq, int k,
   Plan pl;
   const int G = Hq / c->num_kv_heads;
   const int64_t T = p->num_queries, S = p->num_seqs, H = c->num_kv_heads;
+  const bool grid = row_grid(p, c).rows > 0;
   auto tiles = [](int64_t rows, int64_t per) { return (rows + per - 1) / per; };
   if (k > 0) {
-    pick_rows(pl.own, G);
+    pick_rows(pl.own, G, grid);
     const int64_t units = T * tiles(G, pl.own.rows) * H;
     split_keys(pl.own, units, k, k);
     pl.own.bound = units * pl.own.nch;
   } else {
     const int64_t ng = share ? share->num_groups : 0, longest = ng ? share->max_len : 0;
     const int64_t per_seq = tiles(T, S) * G;
-    pick_rows(pl.own, per_seq);
+    pick_rows(pl.own, per_seq, grid);
     // what the prefixes hold is not read per sequence
     const int64_t keys = std::max<int64_t>(p->total_keys - (S - ng) * longest, p->total_keys / 16) / S + 1;
     split_keys(pl.own, S * tiles(per_seq, pl.own.rows) * H, keys, p->max_seq_len);
     pl.own.bound = (T * G / pl.own.rows + S) * H * pl.own.nch;
     if (ng && longest > 0) {
       const int64_t per_group = tiles(T, ng) * G;
-      pick_rows(pl.shared, per_group);
+      pick_rows(pl.shared, per_group, grid);
       split_keys(pl.shared, ng * tiles(per_group, pl.shared.rows) * H, longest, longest);
       pl.shared.bound = (T * G / pl.shared.rows + ng) * H * pl.shared.nch;
     }
@@ -693,6 +732,22 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   const bool cap = opts->softcap > 0.f;
   a.scale2 = cap ? 2.f * opts->scale / opts->softcap * kLog2e : opts->scale * kLog2e;
   a.cap2 = cap ? opts->softcap * kLog2e : 0.f;
+  const RowGrid grid = row_grid(p, c);
+  if (grid.rows) {
+    // a stride that nothing is multiplied by need not be a multiple of the unit
+    a.unit = grid.unit;
+    a.page_rows = (int)(c->page_stride / grid.unit);
+    a.token_rows = (int)(c->token_stride / grid.unit);
+    a.head_rows = (int)(c->head_stride / grid.unit);
+    a.map_rows = (int)grid.rows;
+    // Boxes of up to 64 consecutive rows of a page, at least the eight of a
+    // swizzle pattern; where the tokens are packed they start anywhere.
+    const int box = c->page_table ? std::gcd(c->page_size, 64) : 64;
+    const bool apart = c->token_stride > 0 && (c->num_kv_heads == 1 || c->head_stride > 0) &&
+                       (!c->page_table || c->num_pages <= 1 || c->page_stride > 0);
+    a.box = box >= 8 && apart ? box : 0;
+    a.box_align = a.box && c->page_table ? box : 1;
+  }
   a.S = p->num_seqs;
   a.T = p->num_queries;
   a.Hq = Hq;

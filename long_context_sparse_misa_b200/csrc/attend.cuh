@@ -30,6 +30,9 @@ struct AttendArgs {
   float cap2;          // cap * log2(e), or 0
   int S, T, Hq, Hkv, G, k, ng, max_shared, max_seq_len;
   int chunk, nch_max;  // keys of an item; most items along the keys
+  int64_t unit;        // the tensor core kernel's rows: elements between them (divides every stride),
+  int page_rows, token_rows, head_rows, map_rows;  // strides in rows, and how many there are
+  int box, box_align;  // rows of a box of consecutive ones (0: none), and what its first is a multiple of
   int slot0, nslots;   // this launch's first slot of a row's partial results; slots of a row
 };
 
@@ -52,13 +55,97 @@ __device__ __forceinline__ float rcp(float x) {
   return r;
 }
 
-// Product -> exponent of 2, without the bias.  cap tanh(u) is formed as
-// cap - 2 cap / (e^{2u} + 1): exact at both ends (e^{2u} = inf and 0), and off
-// by a rounding of the cap near zero, where tanh.approx would be off by 2^-11.
-template <bool PLAIN>
-__device__ __forceinline__ float exponent(float s, const AttendArgs& a) {
-  if (!PLAIN && a.cap2 > 0.f) return fmaf(-2.f * a.cap2, rcp(ex2(s * a.scale2) + 1.f), a.cap2);
-  return s * a.scale2;
+// What is done to a product before the softmax, a kernel each: a cap's two
+// more special-function results per element would otherwise be paid by all.
+enum Change { kScaled = 0, kBiased = 1, kCapped = 2 /* and a bias, if there are slopes */ };
+
+// Three-way maximum; NaN if any is.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+// Pairs of fp32 values in one 64-bit register pair, for the packed instructions.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// 2^x of a pair on the multiply-add pipe, for a share of the exponentials
+// where the special-function pipe (16 a cycle and SM) would bound the softmax.
+// 2^x = 2^n 2^r, n the nearest integer, r in [-1/2, 1/2]; 2^r = 1 + r q(r) with
+// q the polynomial of degree 4 whose largest relative error is least (2^-23.3,
+// found by weighted least squares; 2^-22.3 as evaluated).  x <= 127.  Below
+// -127 (and at -infinity) the result is exactly 0; a NaN is not kept.
+__device__ __forceinline__ uint64_t ex2_poly(uint64_t x) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+  float x0, x1, t0, t1, p0, p1;
+  unpair(x, x0, x1);
+  x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+  const uint64_t t = add2(x, pair(kRound, kRound));
+  const uint64_t r = fma2(add2(t, pair(-kRound, -kRound)), pair(-1.f, -1.f), x);
+  uint64_t p = fma2(pair(0x1.5bba14p-10f, 0x1.5bba14p-10f), r, pair(0x1.3cea88p-7f, 0x1.3cea88p-7f));
+  p = fma2(p, r, pair(0x1.c6b752p-5f, 0x1.c6b752p-5f));
+  p = fma2(p, r, pair(0x1.ebf9bcp-3f, 0x1.ebf9bcp-3f));
+  p = fma2(p, r, pair(0x1.62e42ap-1f, 0x1.62e42ap-1f));
+  p = fma2(p, r, pair(1.f, 1.f));
+  unpair(t, t0, t1);
+  unpair(p, p0, p1);
+  return pair(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
+              __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23)));
+}
+
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// Four products -> capped exponents of 2.  cap tanh(u) is formed as
+// cap - 2 cap / (e^{2u} + 1): exact at both ends, and off by a rounding of the
+// cap near zero, where tanh.approx would be off by 2^-11.  The four quotients
+// share one reciprocal (1 / x = y z w / (x y z w)); e^{2u} is held at 2^30 (tanh
+// is 1 to fp32 from 2^26 on), so that the product stays in range.  A NaN makes
+// all four NaN: places that a row does not see are set to 0 before.
+__device__ __forceinline__ void cap4(float& x0, float& x1, float& x2, float& x3, const AttendArgs& a) {
+  const uint64_t sc = pair(a.scale2, a.scale2), one = pair(1.f, 1.f), c = pair(a.cap2, a.cap2);
+  float y0, y1, y2, y3, m0, m1;
+  unpair(mul2(pair(x0, x1), sc), y0, y1);
+  unpair(mul2(pair(x2, x3), sc), y2, y3);
+  const uint64_t e01 = add2(pair(ex2(min_nan(y0, 30.f)), ex2(min_nan(y1, 30.f))), one);
+  const uint64_t e23 = add2(pair(ex2(min_nan(y2, 30.f)), ex2(min_nan(y3, 30.f))), one);
+  unpair(mul2(e01, e23), m0, m1);
+  const float r = rcp(m0 * m1) * (-2.f * a.cap2);
+  const uint64_t q = pair(r * m1, r * m0);  // -2 cap / (e0 e2), -2 cap / (e1 e3)
+  unpair(fma2(q, e23, c), x0, x1);
+  unpair(fma2(q, e01, c), x2, x3);
+}
+
+// Row of the cache seen as [map_rows, D], head 0, or -1: place `off` of page `pg`, or, packed,
+// token `pos` of the sequence whose first is `first`.
+__device__ __forceinline__ int cache_unit(const AttendArgs& a, int64_t first, int pos, int pg, int off) {
+  if (a.c.table) return pg < 0 || pg >= a.c.num_pages ? -1 : pg * a.page_rows + off * a.token_rows;
+  const int64_t r = first + pos;
+  return r >= 0 && r < a.c.total_keys ? (int)r * a.token_rows : -1;
 }
 
 // Tokens of sequence s, at most what the launch was sized for.

@@ -17,10 +17,16 @@
 // 2^8 since its reference was taken (the result does not depend on the
 // reference), which after the first tiles hardly happens.
 //
-// Warps 0-3 gather key and value rows by cp.async into a ring of 128-row
-// tiles, 128-byte swizzled; warps 4-7 and 8-11 are the softmax of A and B;
-// warp 12 issues the products (one thread).  Blocks are persistent; the
-// gathering warps run ahead into the next item.
+// Warps 0-3 and 4-7 are the softmax of A and B.  Warp 8 issues the products
+// (one thread).  Warp 9 finds where the rows of each tile lie; warps 10, 11
+// (keys) and 12, 13 (values) fetch them into a ring of 128-row tiles, 128-byte
+// swizzled: a tile of whole pages by TMA boxes, any other, and a selection, by
+// TMA gathers of four rows (a row that does not exist is out of the map's bounds
+// and comes as zeros).  A thread issues a gather in about 35 cycles, so two share
+// a tile; the copies themselves go on at more than twice what four issue (12.6
+// TB/s from L2 by four threads an SM, 17.9 by six).  Warp 14 looks over value
+// tiles that only some rows see (cut_infinite).  Blocks are persistent, and the
+// fetching warps run ahead into the next item.
 #include <type_traits>
 
 #include "attend.cuh"
@@ -31,24 +37,34 @@ namespace {
 constexpr int kTcThreads = 512;
 constexpr int kTile = 128;          // keys of a tile, rows of a stream
 constexpr float kSlack = 8.f;       // log2 of how far a row's maximum may outgrow its reference
+constexpr int kPrep = 2;            // tiles whose rows have been found and not been fetched
 constexpr int kKeep = 8;            // tiles whose key masks are kept
 
 template <int D, bool PAIR>
 struct Tc {
+  static constexpr int lead = PAIR ? 1 : 2;                // key tiles fetched before their values
   static constexpr int halves = D / 64;
   static constexpr int half = kTile * 128;                 // 64 dims of a tile
   static constexpr int tile = half * halves;
   static constexpr int q_tiles = PAIR ? 2 : 1;
   static constexpr int slots = D == 128 ? 5 : 10;
   static constexpr int off_ring = q_tiles * tile;
-  static constexpr int off_key = off_ring + slots * tile;  // positions, selected mode with a bias
-  static constexpr int off_inv = off_key + (PAIR ? 0 : kKeep * kTile * 4);
+  static constexpr int off_far = off_ring + slots * tile;  // distances, selected mode with a bias
+  static constexpr int off_inv = off_far + (PAIR ? 0 : kKeep * kTile * 4);
   static constexpr int off_ml = off_inv + kKeep * 16;
-  static constexpr int off_bar = off_ml + (PAIR ? 0 : 2 * kTile * 8);
-  static constexpr int bars = 2 * slots + 9;
+  static constexpr int off_rows = off_ml + (PAIR ? 0 : 2 * kTile * 8);
+  static constexpr int off_bar = off_rows + kPrep * kTile * 4;
+  static constexpr int bars = 2 * slots + 13 + 2 * kPrep;
   static constexpr int off_sum = off_bar + bars * 8;
   static constexpr int bytes = off_sum + 16 + (kScan + 1 + kScan / 32) * 4 + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory of a block");
 };
+
+// Which pairs of exponentials are computed by ex2_poly.
+template <int KIND>
+__host__ __device__ constexpr bool poly_pair(int j) {
+  return KIND == kCapped && j % 2 == 1;
+}
 
 template <typename E>
 __host__ __device__ constexpr uint32_t tc_idesc(int N, bool b_mn) {
@@ -96,6 +112,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 struct Span {
   Item it;
   int k0, k1, n;  // keys, and tiles of them
+  int cut;        // the first tile that holds keys which not all rows see
   int near;       // every row that sees anything sees the keys up to this one
   bool live;
 };
@@ -117,7 +134,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const int* sums, in
     }
   } else {
     find_item<MODE>(a, ROWS, sums, (int)(w / a.Hkv), s.it);
-    s.k0 = s.it.k0;
+    s.k0 = s.it.k0 & ~(a.box_align - 1);  // tiles start where a box can; keys before it.k0 are masked
     s.k1 = s.it.k1;
     const int q0 = s.it.qb + s.it.r0 / a.G, q1 = s.it.qb + (s.it.r0 + s.it.nrows - 1) / a.G;
     const int len = MODE == kOwn ? seq_len(a, s.it.seq) : 0x7fffffff;
@@ -133,18 +150,67 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const int* sums, in
     // no key behind the furthest query of the item
     if constexpr (MODE == kOwn) s.k1 = min(s.k1, __reduce_max_sync(0xffffffffu, far) + 1);
   }
-  s.n = s.live && s.k1 > s.k0 ? (s.k1 - s.k0 + kTile - 1) / kTile : 0;
+  s.n = s.live && s.k1 > s.it.k0 ? (s.k1 - s.k0 + kTile - 1) / kTile : 0;
+  s.cut = s.n;
+  if (MODE != kSelected && s.near < s.k1 - 1) s.cut = s.near < s.k0 ? 0 : min(s.n, (s.near + 1 - s.k0) / kTile);
   return s;
 }
 
-// Order of the ring.  pair: K0 V0 K1 V1 ..; split: K0 K1 V0 K2 V1 K3 .. V(n-1).
+// Order of the ring: `lead` key tiles, then value tile t and key tile t + lead
+// in turn.  Place of value tile t among an item's 2 n tiles:
 template <bool PAIR>
-__device__ __forceinline__ int place_k(int t) { return PAIR ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
-template <bool PAIR>
-__device__ __forceinline__ int place_v(int t, int n) { return PAIR ? 2 * t + 1 : (t == n - 1 ? 2 * n - 1 : 2 * t + 2); }
+__device__ __forceinline__ int place_v(int t, int n) {
+  constexpr int lead = PAIR ? 1 : 2;
+  return t + min(t + lead, n);
+}
 
-template <typename E, int D, int MODE, bool PAIR, bool PLAIN>
-__global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_constant__ AttendArgs a) {
+template <bool PAIR>
+__device__ __forceinline__ int place_k(int t) {
+  constexpr int lead = PAIR ? 1 : 2;
+  return t < lead ? t : 2 * t - lead + 1;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// A load that stays where it is written, ahead of copies that it does not depend on.
+__device__ __forceinline__ int load_early(const int32_t* p) {
+  int r;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+
+// Four rows of 64 elements, from element x of each on.
+__device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* bar, void* dst, int x, const int4& r) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+      : "memory");
+}
+
+// A box of rows from place `off` of a page on, 64 elements of each from element x on.
+__device__ __forceinline__ void tma_box(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int off, int head,
+                                        int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(off), "r"(head), "r"(page)
+      : "memory");
+}
+
+// rows: the cache as [map_rows, D], for gathers of any rows; boxes: as
+// [pages, heads, page, D], for runs of `box` rows of one page.
+struct TcMaps {
+  CUtensorMap rows[2], boxes[2];  // keys, values
+};
+
+template <typename E, int D, int MODE, bool PAIR, int KIND>
+__global__ void __launch_bounds__(kTcThreads, 1)
+attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ TcMaps maps) {
   pdl_wait_then_release();
   using L = Tc<D, PAIR>;
   constexpr int kRows = kTile * L::q_tiles;
@@ -152,23 +218,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + L::off_ring;
-  int* s_key = reinterpret_cast<int*>(smem + L::off_key);
+  float* s_far = reinterpret_cast<float*>(smem + L::off_far);
   uint32_t* s_inv = reinterpret_cast<uint32_t*>(smem + L::off_inv);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::off_ml);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::off_bar);
   uint64_t* empty = full + kSlots;
   uint64_t* s_full = empty + kSlots;
   uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
+  uint64_t* o_full = p_full + 4;
   uint64_t* q_full = o_full + 2;
   uint64_t* ml_full = q_full + 1;
   uint64_t* drain = ml_full + 1;
+  uint64_t* cut_ask = drain + 1;
+  uint64_t* cut_done = cut_ask + 1;
+  uint64_t* prep_full = cut_done + 1;
+  uint64_t* prep_empty = prep_full + kPrep;
+  int4* s_rows = reinterpret_cast<int4*>(smem + L::off_rows);  // a tile's rows, or its boxes' places and pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::off_sum);
   int* abort = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   volatile int* s_cut = abort + 1;  // something was cut out of a value tile of this block
+  volatile int* s_boxed = abort + 2;  // bit i: entry i of s_rows holds boxes
   int* s_sum = abort + 3;
   int total;
   if constexpr (MODE == kSelected) {
@@ -180,22 +252,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], 4);
+      mbar_init(&full[i], 2);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(q_full, 8);
     mbar_init(ml_full, 8);
     mbar_init(drain, 1);
+    mbar_init(cut_ask, 1);
+    mbar_init(cut_done, 1);
+    for (int i = 0; i < kPrep; ++i) {
+      mbar_init(&prep_full[i], 1);
+      mbar_init(&prep_empty[i], 4);
+    }
+    *s_boxed = 0;
     *abort = 0;
     *s_cut = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -204,114 +284,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp < 4) {
-    // ------------------------------------------------------------ gathering
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    constexpr int kChunks = D / 8, kPer = 32 / kChunks;
-    const int c = lane % kChunks, sub = lane / kChunks;
-    int cnt = 0, told = 0;  // tiles issued and announced
-    int seen = 0;           // key tiles of the items before
-    bool ok = true;
-    auto announce = [&](int upto) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (; told < upto; ++told) mbar_arrive(&full[told % kSlots]);
-      told = upto;
-    };
-    for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      const Span s = span_of<MODE, kRows>(a, s_sum, w);
-      if (s.n == 0) continue;
-      const int64_t head = s.it.h * a.c.head_stride;
-      const int pos = MODE == kSelected ? __ldg(a.q_pos + s.it.qb) : 0;
-      // lane l knows key 32 warp + l of a tile
-      auto key_of = [&](int t) -> int {
-        const int j = s.k0 + t * kTile + warp * 32 + lane;
-        if (t >= s.n || j >= s.k1) return -1;
-        return MODE == kSelected ? __ldg(a.idx + (int64_t)s.it.qb * a.k + j) : j;
-      };
-      auto row_of = [&](int key) -> int64_t {
-        if (key < 0) return -1;
-        if (MODE == kSelected && key > pos) {
-          set_status(a.status, MISA_STATUS_BAD_INPUT);
-          return -1;
-        }
-        const int64_t r = cache_row(a.c, s.it.seq, key);
-        if (r < 0) set_status(a.status, MISA_STATUS_BOUNDS);
-        return r;
-      };
-      int key_cur = key_of(0), key_next = key_of(1);
-      int64_t row_prev = -1, row_cur = row_of(key_cur);
-      int t_k = 0;  // next tile whose keys are loaded
-      for (int m = 0; m < 2 * s.n; ++m) {
-        bool is_k;
-        int t;
-        if (PAIR) {
-          is_k = (m & 1) == 0;
-          t = m >> 1;
-        } else {
-          is_k = m == 0 || ((m & 1) && (m + 1) / 2 < s.n);
-          t = is_k ? (m + 1) / 2 : (m == 2 * s.n - 1 ? s.n - 1 : (m - 2) / 2);
-        }
-        const int slot = cnt % kSlots;
-        if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[slot], ((cnt / kSlots) & 1) ^ 1))) {
-          cp_async_wait_group<0>();  // what has been issued is announced before waiting
-          announce(cnt);
-          if (!warp_wait(&empty[slot], ((cnt / kSlots) & 1) ^ 1, abort, a.status)) { ok = false; break; }
-        }
-        int64_t row;
-        if (is_k) {
-          if (t_k > 0) {
-            row_prev = row_cur;
-            key_cur = key_next;
-            row_cur = row_of(key_cur);
-            key_next = key_of(t + 1);
-          }
-          ++t_k;
-          row = row_cur;
-          const int j = s.k0 + t * kTile + warp * 32 + lane;
-          // a key that does not exist; those behind k1 are told by their number alone
-          const uint32_t inv = __ballot_sync(0xffffffffu, row < 0 && (MODE == kSelected || j < s.k1));
-          if (lane == 0) s_inv[((seen + t) % kKeep) * 4 + warp] = inv;
-          if (MODE == kSelected && !PLAIN) s_key[((seen + t) % kKeep) * kTile + warp * 32 + lane] = key_cur;
-        } else {
-          row = t == t_k - 1 ? row_cur : row_prev;
-        }
-        uint8_t* dst = ring + slot * L::tile + (c >> 3) * L::half;
-        const uint16_t* base = (is_k ? a.c.k : a.c.v) + head + c * 8;
-#pragma unroll 4
-        for (int u = 0; u < 32 / kPer; ++u) {
-          const int r = u * kPer + sub;
-          const int64_t off = __shfl_sync(0xffffffffu, row, r);
-          const int rr = warp * 32 + r;
-          cp_async_16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), base + (off < 0 ? -head : off), off >= 0);
-        }
-        cp_async_commit();
-        ++cnt;
-        if (MODE != kSelected && !is_k && s.k0 + t * kTile + kTile - 1 > s.near) {
-          // keys that not every row sees: each lane looks over what it copied
-          cp_async_wait_group<0>();
-          bool cut = false;
-#pragma unroll 4
-          for (int u = 0; u < 32 / kPer; ++u) {
-            const int rr = warp * 32 + u * kPer + sub;
-            if (s.k0 + t * kTile + rr > s.near)
-              cut |= cut_infinite<E>(reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)));
-          }
-          if (cut) *s_cut = 1;
-          announce(cnt);
-        }
-        cp_async_wait_group<2>();
-        if (cnt - 2 > told) announce(cnt - 2);
-      }
-      seen += s.n;
-    }
-    cp_async_wait_group<0>();
-    if (cnt > told) announce(cnt);
-  } else if (warp < 12) {
+  if (warp < 8) {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    const int x = (warp - 4) >> 2;               // stream
+    const int x = warp >> 2;                     // stream
     const int r = ((warp & 3) << 5) + lane;      // row of the stream: its TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
@@ -343,6 +319,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
         uint4 v[kC];
 #pragma unroll
         for (int i = 0; i < kC; ++i) v[i] = real ? __ldg(src + c0 + i) : make_uint4(0, 0, 0, 0);
+        if (KIND == kScaled && a.scale2 < 0.f) {  // the softmax works with a positive scale
+#pragma unroll
+          for (int i = 0; i < kC; ++i)
+            v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
+        }
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
           const int c = c0 + i;
@@ -354,15 +335,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
         if (lane == 0) mbar_arrive(q_full);
       }
       float slope = 0.f;
-      const bool bias = !PLAIN && a.slopes;
+      const bool bias = KIND == kBiased || (KIND == kCapped && a.slopes);
       if (bias) slope = __ldg(a.slopes + h) * kLog2e;
-      const float sc = PLAIN ? fabsf(a.scale2) : 1.f;
-      const bool flip = PLAIN && a.scale2 < 0.f;
+      // at least 1e-30, so that a scale of 0 keeps a masked -inf what it is
+      const float sc = KIND == kScaled ? fmaxf(fabsf(a.scale2), 1e-30f) : 1.f;
       // contiguous keys: the last one that this row sees
       const int lim = MODE == kSelected ? 0x7fffffff : min(pos, s.k1 - 1);
       const int least = __reduce_min_sync(0xffffffffu, lim);
       const int mine = PAIR ? s.n : (s.n + 1 - x) / 2;
-      float ref = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float ref = -INFINITY;
+      uint64_t l01 = pair(0.f, 0.f);  // the row's sum: even and odd keys
+      const uint64_t sc2 = pair(sc, sc);
       for (int i = 0; i < mine; ++i) {
         const int tile = PAIR ? i : 2 * i + x;
         const int base = s.k0 + tile * kTile;
@@ -375,75 +358,77 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) reg_fence32(v[q]);
-        if (flip) {
+        // what this row does not see gets `value`
+        const int last = lim - base;  // contiguous keys: columns up to this one are seen
+        const uint4 inv = *reinterpret_cast<const uint4*>(s_inv + ((first_tile + tile) % kKeep) * 4);
+        auto mask = [&](float value) {
+          if (MODE != kSelected && base + kTile - 1 > least) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] = -v[q][j];
-        }
-        if constexpr (!PLAIN) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] = exponent<false>(v[q][j], a);
-          if (bias) {
-            if constexpr (MODE == kSelected) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const int4 kp = *reinterpret_cast<const int4*>(s_key + ((first_tile + tile) % kKeep) * kTile + q * 32 + j);
-                  v[q][j] = fmaf(-slope, (float)(pos - kp.x), v[q][j]);
-                  v[q][j + 1] = fmaf(-slope, (float)(pos - kp.y), v[q][j + 1]);
-                  v[q][j + 2] = fmaf(-slope, (float)(pos - kp.z), v[q][j + 2]);
-                  v[q][j + 3] = fmaf(-slope, (float)(pos - kp.w), v[q][j + 3]);
-                }
-            } else {
-              const float first = (float)(pos - base);
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[q][j] = fmaf(-slope, first - (float)(q * 32 + j), v[q][j]);
-            }
+              for (int j = 0; j < 32; ++j)
+                if (q * 32 + j > last) v[q][j] = value;
           }
-        }
-        if (MODE != kSelected && base + kTile - 1 > least) {
-          const int last = lim - base;  // columns up to this one are seen
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (q * 32 + j > last) v[q][j] = -INFINITY;
-        }
-        {
-          const uint4 inv = *reinterpret_cast<const uint4*>(s_inv + ((first_tile + tile) % kKeep) * 4);
           if (inv.x | inv.y | inv.z | inv.w) {
             const uint32_t word[4] = {inv.x, inv.y, inv.z, inv.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (word[q] >> j & 1u) v[q][j] = -INFINITY;
+                if (word[q] >> j & 1u) v[q][j] = value;
           }
+        };
+        if constexpr (KIND == kCapped) {
+          mask(0.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) cap4(v[q][j], v[q][j + 1], v[q][j + 2], v[q][j + 3], a);
         }
-        float top = -INFINITY;
+        if (bias) {
+          const uint64_t mul = KIND == kCapped ? pair(1.f, 1.f) : pair(a.scale2, a.scale2);
+          const float* far = s_far + ((first_tile + tile) % kKeep) * kTile;
+          const float first = -slope * (float)(pos - base);
+          const uint64_t step = pair(2.f * slope, 2.f * slope), minus = pair(-slope, -slope);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              // slope times the distance: for contiguous keys three steps from an exact start
+              uint64_t b[4];
+              if constexpr (MODE == kSelected) {
+                const float4 d = *reinterpret_cast<const float4*>(far + q * 32 + j);
+                const float4 e = *reinterpret_cast<const float4*>(far + q * 32 + j + 4);
+                b[0] = mul2(minus, pair(d.x, d.y)), b[1] = mul2(minus, pair(d.z, d.w));
+                b[2] = mul2(minus, pair(e.x, e.y)), b[3] = mul2(minus, pair(e.z, e.w));
+              } else {
+                b[0] = pair(fmaf(slope, (float)(q * 32 + j), first), fmaf(slope, (float)(q * 32 + j + 1), first));
+#pragma unroll
+                for (int u = 1; u < 4; ++u) b[u] = add2(b[u - 1], step);
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                unpair(fma2(pair(v[q][j + 2 * u], v[q][j + 2 * u + 1]), mul, b[u]), v[q][j + 2 * u], v[q][j + 2 * u + 1]);
+            }
+        }
+        mask(-INFINITY);
+        float top4[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float m0 = v[q][0], m1 = v[q][1];
+          top4[q] = v[q][0];
 #pragma unroll
-          for (int j = 2; j < 32; j += 2) {
-            m0 = fmaxf(m0, v[q][j]);
-            m1 = fmaxf(m1, v[q][j + 1]);
-          }
-          top = fmaxf(top, fmaxf(m0, m1));
+          for (int j = 1; j < 31; j += 2) top4[q] = max3(top4[q], v[q][j], v[q][j + 1]);
+          top4[q] = max3(top4[q], v[q][31], v[q][31]);
         }
+        float top = max3(max3(top4[0], top4[1], top4[2]), top4[3], top4[3]);
         top *= sc;  // sc > 0: -inf stays
-        const bool grow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+        // an infinite or undefined exponent makes the row's results undefined
+        if (!(top < INFINITY)) top = __int_as_float(0x7fffffff);
+        const bool grow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY) || top != top;
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(ref - top) : 1.f;  // 0 while nothing had been seen
           if (grow) ref = top;
-          l0 *= f;
-          l1 *= f;
+          l01 = mul2(l01, pair(f, f));
           if (i > 0) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -459,28 +444,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
           }
         }
         const float minus = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t minus2 = pair(minus, minus);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t p[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            float& e0 = v[2 * q + (j >> 4)][(j & 15) * 2];
-            float& e1 = v[2 * q + (j >> 4)][(j & 15) * 2 + 1];
-            e0 = ex2(fmaf(e0, sc, minus));
-            e1 = ex2(fmaf(e1, sc, minus));
-            l0 += e0;
-            l1 += e1;
+            uint64_t e = pair(v[2 * q + (j >> 4)][(j & 15) * 2], v[2 * q + (j >> 4)][(j & 15) * 2 + 1]);
+            float e0, e1;
+            e = KIND == kScaled ? fma2(e, sc2, minus2) : add2(e, minus2);
+            if (poly_pair<KIND>(j)) {
+              e = ex2_poly(e);
+              unpair(e, e0, e1);
+            } else {
+              unpair(e, e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              e = pair(e0, e1);
+            }
+            l01 = add2(l01, e);
             // the weights' one rounding to the cache's type; their sum keeps fp32
             p[j] = pack2(e0, e1, tag);
           }
           tmem_st32(tS + q * 32, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + q]);  // half of the keys
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
+      float l0, l1;
+      unpair(l01, l0, l1);
       float l = l0 + l1;
       if (mine > 0) {
         if (!warp_wait(&o_full[x], n_o & 1, abort, a.status)) break;
@@ -518,7 +513,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
       const int d0 = PAIR ? 0 : x * kCols;
       const uint32_t ta = tmem + lanes + 256 + (PAIR ? x * 128 : 0) + d0, tb = tmem + lanes + 384 + d0;
       // values cut out of a tile that this row does see (only rows behind `near` can)
-      const int cut0 = max(s.k0, s.near + 1);
+      const int cut0 = max(s.it.k0, s.near + 1);
       const bool cut = MODE != kSelected && s.n > 0 && real && cut0 <= lim && *s_cut;
       const bool any_a = PAIR ? mine > 0 : s.n > 0, any_b = !PAIR && s.n > 1;
 #pragma unroll 1
@@ -563,93 +558,299 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const __grid_c
       tc_fence_before();
     }
   } else {
-    // ------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 12) {
-      const uint32_t idesc_s = tc_idesc<E>(kTile, false), idesc_o = tc_idesc<E>(D, true);
+    if (warp == 9) {
+      // ---------------------------------------------------------- finding rows
+      // lane l finds keys 4 l .. 4 l + 3 of a tile
+      int seen = 0;  // key tiles of the items before
+      bool ok = true;
+      for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+        const Span s = span_of<MODE, kRows>(a, s_sum, w);
+        if (s.n == 0) continue;
+        const int head = s.it.h * a.head_rows;
+        const int64_t first_row = a.c.table ? 0 : __ldg(a.c.ko + s.it.seq);  // packed
+        const int pos = MODE == kSelected ? __ldg(a.q_pos + s.it.qb) : 0;
+        const int32_t* list = a.idx + (int64_t)s.it.qb * a.k;
+        const int32_t* table = a.c.table + s.it.seq * a.c.table_stride;
+        auto keys_of = [&](int t, int (&key)[4]) {
+          const int j = s.k0 + t * kTile + lane * 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            key[i] = -1;
+            if (t < s.n && j + i >= s.it.k0 && j + i < s.k1) key[i] = MODE == kSelected ? load_early(list + j + i) : j + i;
+          }
+        };
+        // Page and place in it of each key, and the page table's entry, read whether it is needed
+        // or not: four loads in flight.  (One test of the page size: divisions cost more than the copies.)
+        auto pages_of = [&](const int (&key)[4], int (&page)[4], int (&off)[4]) {
+          if (!a.c.table) return;
+          if (a.c.page_shift >= 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              page[i] = max(key[i], 0) >> a.c.page_shift;
+              off[i] = max(key[i], 0) & (a.c.page_size - 1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              page[i] = max(key[i], 0) / a.c.page_size;
+              off[i] = max(key[i], 0) - page[i] * a.c.page_size;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) page[i] = page[i] < a.c.pages_per_seq ? load_early(table + page[i]) : -1;
+        };
+        // a tile's keys and pages, and the next one's keys
+        int key[4], page[4] = {0, 0, 0, 0}, off[4] = {0, 0, 0, 0}, next[4];
+        keys_of(0, key);
+        pages_of(key, page, off);
+        keys_of(1, next);
+        for (int t = 0; t < s.n; ++t) {
+          int row[4];
+          uint32_t bad = 0, none = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool ahead = MODE == kSelected && key[i] > pos;
+            const int r = cache_unit(a, first_row, max(key[i], 0), page[i], off[i]);
+            const bool there = key[i] >= 0 && !ahead && r >= 0;
+            if (key[i] >= 0 && !there) bad |= ahead ? MISA_STATUS_BAD_INPUT : MISA_STATUS_BOUNDS;
+            row[i] = there ? head + r : a.map_rows;  // out of the map's bounds: zeros
+            // keys that do not exist; those behind k1 of contiguous ones are told by their number alone
+            if (!there && (MODE == kSelected || s.k0 + t * kTile + lane * 4 + i < s.k1)) none |= 1u << i;
+          }
+          if (bad) set_status(a.status, bad);
+          uint32_t word = 0;
+          const bool whole = !__any_sync(0xffffffffu, none != 0);
+          if (!whole) {
+            word = none << (4 * (lane & 7));
+            word |= __shfl_xor_sync(0xffffffffu, word, 1);
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+          }
+          const bool boxed = MODE != kSelected && a.box > 0 && whole && s.k0 + (t + 1) * kTile <= s.k1;
+          const float4 far = make_float4(pos - key[0], pos - key[1], pos - key[2], pos - key[3]);
+          const int2 place = a.c.table ? make_int2(off[0], page[0]) : make_int2((int)first_row + key[0], 0);
+          // the loads of the tiles to come run while this one waits
+#pragma unroll
+          for (int i = 0; i < 4; ++i) key[i] = next[i];
+          pages_of(key, page, off);
+          keys_of(t + 2, next);
+          const int entry = (seen + t) % kPrep, keep = (seen + t) % kKeep;
+          ok = warp_wait(&prep_empty[entry], (((seen + t) / kPrep) & 1) ^ 1, abort, a.status);
+          if (!ok) break;
+          if ((lane & 7) == 0) s_inv[keep * 4 + (lane >> 3)] = word;
+          if (MODE == kSelected && KIND != kScaled) *reinterpret_cast<float4*>(s_far + keep * kTile + lane * 4) = far;
+          int4* rows = s_rows + entry * 32;
+          if (!boxed) rows[lane] = make_int4(row[0], row[1], row[2], row[3]);
+          else if (lane * 4 % a.box == 0) reinterpret_cast<int2*>(rows)[lane * 4 / a.box] = place;
+          if (lane == 0) *s_boxed = (*s_boxed & ~(1 << entry)) | (boxed ? 1 << entry : 0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&prep_full[entry]);
+        }
+        seen += s.n;
+      }
+    } else if (warp >= 10 && warp < 14) {
+      // ---------------------------------------------------------- fetching: keys 10, 11, values 12, 13
+      // each warp half of a tile's rows; elect, not lane == 0 (see below)
+      const bool is_v = warp >= 12;
+      const int half = warp & 1;
+      int cnt = 0;   // places of the ring taken by the items before
+      int seen = 0;  // tiles of the items before
+      int last = -1;       // the last place filled; bit i of mine: place last - i was filled by this warp
+      uint32_t mine = 0;
+      bool ok = true;
+      for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+        const Span s = span_of<MODE, kRows>(a, s_sum, w);
+        if (elect_one()) {
+          for (int t = 0; t < s.n; ++t) {
+            const int place = cnt + (is_v ? place_v<PAIR>(t, s.n) : place_k<PAIR>(t));
+            const int slot = place % kSlots, entry = (seen + t) % kPrep;
+            ok = mbar_wait(&prep_full[entry], ((seen + t) / kPrep) & 1, abort, a.status) &&
+                 mbar_wait(&empty[slot], ((place / kSlots) & 1) ^ 1, abort, a.status);
+            if (!ok) break;
+            uint64_t* bar = &full[slot];
+            mbar_arrive_expect_tx(bar, L::tile / 2);
+            mine = mine << (place - last) | 1u;
+            last = place;
+            uint8_t* dst = ring + slot * L::tile + half * (L::half / 2);
+            if (MODE != kSelected && (*s_boxed >> entry & 1)) {
+              const int n = kTile / 2 / a.box;
+              const int2* at = reinterpret_cast<const int2*>(s_rows + entry * 32) + half * n;
+              for (int b = 0; b < n; ++b) {
+                const int2 x = at[b];
+#pragma unroll
+                for (int u = 0; u < L::halves; ++u)
+                  tma_box(is_v ? &maps.boxes[1] : &maps.boxes[0], bar, dst + u * L::half + b * a.box * 128, u * 64, x.x,
+                          s.it.h, x.y);
+              }
+            } else {
+              const int4* rows = s_rows + entry * 32 + half * 16;
+#pragma unroll 8
+              for (int g = 0; g < 16; ++g) {
+                const int4 r = rows[g];
+#pragma unroll
+                for (int u = 0; u < L::halves; ++u)
+                  tma_gather4(is_v ? &maps.rows[1] : &maps.rows[0], bar, dst + u * L::half + g * 512, u * 64, r);
+              }
+            }
+            mbar_arrive(&prep_empty[entry]);
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        seen += s.n;
+        cnt += 2 * s.n;
+      }
+      // after giving up: this warp's copies still in flight land before the block ends
+      if (!ok && elect_one())
+        for (int i = 0; i < kSlots && i <= last; ++i)
+          if (mine >> i & 1u)
+            mbar_wait(&full[(last - i) % kSlots], ((last - i) / kSlots) & 1, abort, a.status, kDrainCycles, /*drain=*/true);
+    } else if (warp == 8) {
+      // ---------------------------------------------------------- products
       const uint32_t q_addr = smem_u32(smem), ring_addr = smem_u32(ring);
-      int cnt = 0;
-      uint32_t n_q = 0, n_p[2] = {0, 0};
+      constexpr uint32_t idesc_s = tc_idesc<E>(kTile, false), idesc_o = tc_idesc<E>(D, true);
+      int slot = 0, turn = 0;
+      uint32_t n_q = 0, n_p0 = 0, n_p1 = 0, n_cut = 0;
       bool ok = true;
       auto qk = [&](int x, int slot) {
-        const uint32_t qa = q_addr + (PAIR ? x * L::tile : 0), ka = ring_addr + slot * L::tile;
+        const uint64_t qd = sw128_kmajor_desc(q_addr + (PAIR ? x * L::tile : 0));
+        const uint64_t kd = sw128_kmajor_desc(ring_addr + slot * L::tile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * L::half + (kk & 3) * 32;
-          umma_bf16(tmem + x * 128, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), idesc_s, kk > 0);
+          const uint32_t off = ((kk >> 2) * L::half + (kk & 3) * 32) >> 4;
+          umma_bf16(tmem + x * 128, qd + off, kd + off, idesc_s, kk > 0);
         }
       };
-      auto pv = [&](int x, int slot, bool acc) {
-        const uint32_t va = ring_addr + slot * L::tile;
+      auto pv = [&](int x, int slot, bool acc, int half) {
+        const uint64_t vd = sw128_nmajor_desc(ring_addr + slot * L::tile, L::half);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, sw128_nmajor_desc(va + kk * 2048, L::half), idesc_o,
-                  acc || kk > 0);
+        for (int kk = half * kTile / 32; kk < (half + 1) * kTile / 32; ++kk)
+          umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + ((kk * 2048) >> 4), idesc_o, acc || kk > 0);
       };
       for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
         const Span s = span_of<MODE, kRows>(a, s_sum, w);
         if (s.n == 0) continue;
-        if (lane == 0) {
-          auto wait_slot = [&](int place) {
-            const int i = cnt + place;
-            return mbar_wait(&full[i % kSlots], (i / kSlots) & 1, abort, a.status);
+        // elect, not lane == 0: the compiler then knows that one thread issues, and an
+        // instruction costs half the issue slots, which the softmax warps compete for
+        if (elect_one()) {
+          // the next tile of the ring, once it has arrived; -1: given up
+          auto take = [&]() -> int {
+            const int i = slot;
+            if (!mbar_wait(&full[i], turn, abort, a.status)) return -1;
+            if (++slot == kSlots) slot = 0, turn ^= 1;
+            tc_fence_after();
+            return i;
           };
-          const int n0 = PAIR ? s.n : (s.n + 1) / 2, n1 = PAIR ? s.n : s.n / 2;
+          // stream x's tile of keys
+          auto first_product = [&](int x, int k) {
+            qk(x, k);
+            umma_commit(&s_full[x]);
+          };
+          auto second_product = [&](int x, int v, bool acc) {
+            const uint32_t phase = (x ? n_p1++ : n_p0++) & 1;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (!mbar_wait(&p_full[2 * x + half], phase, abort, a.status)) return false;
+              tc_fence_after();
+              pv(x, v, acc, half);
+            }
+            return true;
+          };
+          // value tile t, looked over if not all rows see it
+          auto take_v = [&](int t) -> int {
+            const int v = take();
+            if (v < 0 || MODE == kSelected || t < s.cut) return v;
+            mbar_arrive(cut_ask);
+            if (!mbar_wait(cut_done, n_cut++ & 1, abort, a.status)) return -1;
+            return v;
+          };
           ok = mbar_wait(q_full, n_q & 1, abort, a.status);
           tc_fence_after();
-          for (int i = -1; ok && i < n0; ++i) {
-            for (int x = 0; ok && x < 2; ++x) {
-              const int nx = x ? n1 : n0;
-              if (i >= nx) break;
-              if (i >= 0) {
-                const int t = PAIR ? i : 2 * i + x, place = place_v<PAIR>(t, s.n);
-                ok = wait_slot(place) && mbar_wait(&p_full[x], n_p[x]++ & 1, abort, a.status);
-                if (!ok) break;
-                tc_fence_after();
-                pv(x, (cnt + place) % kSlots, i > 0);
-                if (!PAIR || x == 1) umma_commit(&empty[(cnt + place) % kSlots]);
-              }
-              if (i + 1 < nx) {
-                const int t = PAIR ? i + 1 : 2 * (i + 1) + x, place = place_k<PAIR>(t);
-                if (!(ok = wait_slot(place))) break;
-                tc_fence_after();
-                qk(x, (cnt + place) % kSlots);
-                if (!PAIR || x == 1) umma_commit(&empty[(cnt + place) % kSlots]);
-                umma_commit(&s_full[x]);
-              } else if (i >= 0) {
-                umma_commit(&o_full[x]);
-              }
+          for (int t = 0; ok && t < min(L::lead, s.n); ++t) {
+            const int k = take();
+            if (!(ok = k >= 0)) break;
+            first_product(t & 1, k);
+            if (PAIR) first_product(1, k);
+            umma_commit(&empty[k]);
+          }
+          for (int t = 0; ok && t < s.n; ++t) {
+            const int x = PAIR ? 0 : t & 1;
+            const bool more = t + L::lead < s.n;
+            const int v = take_v(t);
+            if (!(ok = v >= 0 && second_product(x, v, t >= L::lead))) break;
+            int k = 0;
+            if (more) {
+              k = take();
+              if (!(ok = k >= 0)) break;
+              first_product(x, k);
+            } else {
+              umma_commit(&o_full[x]);
             }
+            if (PAIR) {
+              if (!(ok = second_product(1, v, t >= L::lead))) break;
+              umma_commit(&empty[v]);
+              if (more) first_product(1, k);
+              else umma_commit(&o_full[1]);
+            } else {
+              umma_commit(&empty[v]);
+            }
+            if (more) umma_commit(&empty[k]);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = __all_sync(0xffffffffu, ok);
         ++n_q;
-        cnt += 2 * s.n;
       }
-      if (lane == 0) {
+      if (elect_one()) {  // the same thread as above
         // every product must be done before TMEM is given back
         umma_commit(drain);
         mbar_wait(drain, 0, abort, a.status, kDrainCycles, /*drain=*/true);
+      }
+    } else if (warp == 14 && MODE != kSelected) {
+      // ---------------------------------------------------------- looking over values
+      int cnt = 0;
+      uint32_t n_cut = 0;
+      bool ok = true;
+      for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+        const Span s = span_of<MODE, kRows>(a, s_sum, w);
+        for (int t = s.cut; ok && t < s.n; ++t) {
+          const int i = cnt + place_v<PAIR>(t, s.n);
+          ok = warp_wait(cut_ask, n_cut++ & 1, abort, a.status) &&
+               warp_wait(&full[i % kSlots], (i / kSlots) & 1, abort, a.status);
+          if (!ok) break;
+          uint8_t* tile = ring + (i % kSlots) * L::tile;
+          const int from = s.near + 1 - (s.k0 + t * kTile);  // rows of the tile from here on
+          bool cut = false;
+          for (int r = max(from, 0); r < kTile; ++r) {
+            // a row's chunks lie in its 128 bytes of each half, in some order
+            if (lane < D / 8) cut |= cut_infinite<E>(reinterpret_cast<uint4*>(tile + (lane >> 3) * L::half + r * 128) + (lane & 7));
+          }
+          if (cut) *s_cut = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(cut_done);
+        }
+        cnt += 2 * s.n;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 8) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <typename E, int D, int MODE, bool PAIR, bool PLAIN>
-int launch_tc_one(const AttendArgs& a, int64_t bound, cudaStream_t st) {
+template <typename E, int D, int MODE, bool PAIR, int KIND>
+int launch_tc_one(const AttendArgs& a, const TcMaps& maps, int64_t bound, cudaStream_t st) {
   using L = Tc<D, PAIR>;
-  auto kern = attend_tc_kernel<E, D, MODE, PAIR, PLAIN>;
+  auto kern = attend_tc_kernel<E, D, MODE, PAIR, KIND>;
   int rc = set_smem_limit((const void*)kern, L::bytes);
   if (rc) return rc;
   // The roles' register counts add up to what a block of 128-register threads
-  // is launched with; a build that used fewer would wait for registers for good.
+  // is launched with (128 x (192 + 192 + 64 + 64) = 512 x 128); a build that used
+  // fewer would wait for registers for good.
   static const int regs = [&] {
     cudaFuncAttributes fa;
     return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
@@ -662,35 +863,44 @@ int launch_tc_one(const AttendArgs& a, int64_t bound, cudaStream_t st) {
   const unsigned grid = (unsigned)(bound < 1 ? 1 : bound < sms ? bound : sms);
   static const char* const names[] = {"attend_tc", "attend_tc_shared", "attend_tc_selected"};
   ProfScope ps(names[MODE], st);
-  return cuda_fail(launch_pdl(kern, dim3(grid), dim3(kTcThreads), L::bytes, st, a), "attend_tc_kernel");
+  return cuda_fail(launch_pdl(kern, dim3(grid), dim3(kTcThreads), L::bytes, st, a, maps),
+                   "attend_tc_kernel");
 }
 
 template <typename E, int D, int MODE, bool PAIR>
-int launch_tc_kind(const AttendArgs& a, int64_t bound, cudaStream_t st) {
-  // a scale of 0 times a masked -inf: the other form scales before it masks
-  return a.cap2 > 0.f || a.slopes || a.scale2 == 0.f ? launch_tc_one<E, D, MODE, PAIR, false>(a, bound, st)
-                                  : launch_tc_one<E, D, MODE, PAIR, true>(a, bound, st);
+int launch_tc_kind(const AttendArgs& a, const TcMaps& m, int64_t bound, cudaStream_t st) {
+  // a scale of 0 times a masked -inf: the capped form scales before it masks
+  return a.cap2 > 0.f ? launch_tc_one<E, D, MODE, PAIR, kCapped>(a, m, bound, st)
+         : a.slopes   ? launch_tc_one<E, D, MODE, PAIR, kBiased>(a, m, bound, st)
+                      : launch_tc_one<E, D, MODE, PAIR, kScaled>(a, m, bound, st);
 }
 
 template <int MODE, bool PAIR>
-int launch_tc_type(const AttendArgs& a, int dtype, int D, int64_t bound, cudaStream_t st) {
+int launch_tc_type(const AttendArgs& a, const TcMaps& m, int dtype, int D, int64_t bound, cudaStream_t st) {
   if (dtype == MISA_BF16)
-    return D == 128 ? launch_tc_kind<__nv_bfloat16, 128, MODE, PAIR>(a, bound, st)
-                    : launch_tc_kind<__nv_bfloat16, 64, MODE, PAIR>(a, bound, st);
-  return D == 128 ? launch_tc_kind<__half, 128, MODE, PAIR>(a, bound, st)
-                  : launch_tc_kind<__half, 64, MODE, PAIR>(a, bound, st);
+    return D == 128 ? launch_tc_kind<__nv_bfloat16, 128, MODE, PAIR>(a, m, bound, st)
+                    : launch_tc_kind<__nv_bfloat16, 64, MODE, PAIR>(a, m, bound, st);
+  return D == 128 ? launch_tc_kind<__half, 128, MODE, PAIR>(a, m, bound, st)
+                  : launch_tc_kind<__half, 64, MODE, PAIR>(a, m, bound, st);
 }
 
 }  // namespace
 
 // rows: 128 (split) or 256 (pair) rows of an item.
 int launch_attend_tc(const AttendArgs& a, int mode, int rows, int dtype, int D, int64_t bound, cudaStream_t st) {
-  if (mode == kSelected) return launch_tc_type<kSelected, false>(a, dtype, D, bound, st);
+  TcMaps m;
+  for (int i = 0; i < 2; ++i) {
+    const void* base = i ? a.c.v : a.c.k;
+    int rc = make_rows_map(&m.rows[i], base, a.map_rows, D, a.unit, dtype == MISA_FP16);
+    if (!rc && a.box) rc = make_box_map(&m.boxes[i], base, a.c, a.Hkv, D, a.box, dtype == MISA_FP16);
+    if (rc) return rc;
+  }
+  if (mode == kSelected) return launch_tc_type<kSelected, false>(a, m, dtype, D, bound, st);
   if (mode == kShared)
-    return rows == 128 ? launch_tc_type<kShared, false>(a, dtype, D, bound, st)
-                       : launch_tc_type<kShared, true>(a, dtype, D, bound, st);
-  return rows == 128 ? launch_tc_type<kOwn, false>(a, dtype, D, bound, st)
-                     : launch_tc_type<kOwn, true>(a, dtype, D, bound, st);
+    return rows == 128 ? launch_tc_type<kShared, false>(a, m, dtype, D, bound, st)
+                       : launch_tc_type<kShared, true>(a, m, dtype, D, bound, st);
+  return rows == 128 ? launch_tc_type<kOwn, false>(a, m, dtype, D, bound, st)
+                     : launch_tc_type<kOwn, true>(a, m, dtype, D, bound, st);
 }
 
 }  // namespace misa

@@ -68,5 +68,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 int check_batch(const misa_problem_t* p);
 int check_cache(const misa_problem_t* p, const misa_kv_cache_t* c, bool need_v);
 CacheView cache_view(const misa_problem_t* p, const misa_kv_cache_t* c);
+// Tensor map (abi.cu) of the cache as [pages, heads, page, dim], boxes of `box` rows of 64 elements.
+int make_box_map(CUtensorMap* map, const void* base, const CacheView& c, int heads, int dim, int box, bool fp16);
 
 }  // namespace misa

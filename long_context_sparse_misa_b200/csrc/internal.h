@@ -28,6 +28,10 @@ uint32_t* status_ptr();
 // tensor [rows, 128] with a {64, box_rows} box and 128-byte swizzle.
 int make_kmajor_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows);
 
+// The same for attention: `rows` rows of `dim` 16-bit elements, `stride`
+// elements apart, for gathers of four rows of 64 elements.
+int make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim, int64_t stride, bool fp16);
+
 int set_smem_limit(const void* kernel, int bytes);
 
 // Launches `kern` with programmatic dependent launch: its CTAs may be
