@@ -267,6 +267,9 @@ def block_score_topk(prob: Problem, q_r, w_r, m: int, K, Kbar, n_blocks: int, k:
 # ---------------------------------------------------------------- cache and attention
 # These run once per layer and step, on calls of a few microseconds of GPU
 # time: a check costs an attribute or two, and only a refusal builds its text.
+_cuda = _raw_stream = _float32 = _int32 = None  # of torch, from the first KVCache on
+
+
 def _refuse(where: str, what: str):
     raise ValueError(f"{where}: {what}")
 
@@ -287,14 +290,11 @@ def _token_stride(t, where: str, name: str, heads: int, dim: int, like) -> int:
 
 def _on(cache, call, *args, stream):
     """call(*args, stream) with the cache's device current."""
-    import torch
-    index = cache.device.index
-    if torch.cuda.current_device() == index:
-        s = torch.cuda.current_stream() if stream is None else stream
-        return call(*args, s.cuda_stream)
-    with torch.cuda.device(index):
-        s = torch.cuda.current_stream() if stream is None else stream
-        return call(*args, s.cuda_stream)
+    index = cache.index
+    if _cuda.current_device() == index:
+        return call(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    with _cuda.device(index):
+        return call(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
 
 
 class KVCache:
@@ -313,6 +313,9 @@ class KVCache:
 
     def __init__(self, k, v=None, page_table=None):
         import torch
+        global _cuda, _raw_stream, _float32, _int32
+        _cuda, _raw_stream = torch.cuda, torch._C._cuda_getCurrentRawStream
+        _float32, _int32 = torch.float32, torch.int32
         w = "KVCache"
         codes = {torch.bfloat16: 0, torch.float16: 1}
         if not k.is_cuda:
@@ -327,6 +330,7 @@ class KVCache:
             _refuse(w, "v must have k's shape, strides, dtype and device")
         self.k, self.v, self.page_table = k, v, page_table
         self.device, self.dtype, self.heads, self.dim = k.device, k.dtype, k.shape[-2], k.shape[-1]
+        self.index = k.device.index
         c = self.c = _KVCache(k=k.data_ptr() or None, v=None if v is None else v.data_ptr() or None,
                               dtype=codes[k.dtype], num_kv_heads=self.heads, head_dim=self.dim,
                               head_stride=k.stride(-2), token_stride=k.stride(-3))
@@ -401,7 +405,6 @@ def cache_append(prob: Problem, cache: KVCache, k, v=None, q=None, q_out=None, r
                  interleaved: bool = False, stream=None) -> None:
     """Write the problem's query tokens' keys and values into the cache, the
     keys (and q, into q_out) rotated by their positions' rows of ``rope``."""
-    import torch
     w = "cache_append"
     cache._fits(prob, w)
     like, d, heads, T = cache.k, cache.dim, cache.heads, prob.T
@@ -422,7 +425,7 @@ def cache_append(prob: Problem, cache: KVCache, k, v=None, q=None, q_out=None, r
     if k.shape[0] != T or (v is not None and v.shape[0] != T) or (q is not None and q.shape[0] != T):
         _refuse(w, f"k, v and q must have the problem's {T} rows")
     if rope is not None:
-        if (rope.dim() != 2 or rope.dtype != torch.float32 or rope.device != like.device
+        if (rope.dim() != 2 or rope.dtype != _float32 or rope.device != like.device
                 or not rope.is_contiguous()):
             _refuse(w, "rope must be contiguous fp32 [rows, dim] on the cache's device")
         rows, turned = rope.shape
@@ -437,8 +440,7 @@ def cache_append(prob: Problem, cache: KVCache, k, v=None, q=None, q_out=None, r
 def attention_workspace_size(prob: Problem, cache: KVCache, num_q_heads: int, k: int = 0,
                              share: SharedPrefix = None) -> int:
     """Bytes of workspace of attention (k = 0) or attention_selected with lists of k."""
-    import torch
-    with torch.cuda.device(cache.device):
+    with _cuda.device(cache.index):
         n = lib.misa_attention_workspace_size(prob.ref, cache.ref, num_q_heads, k,
                                               _share_ref(share, prob, "attention_workspace_size"))
     if n == 0:
@@ -447,7 +449,6 @@ def attention_workspace_size(prob: Problem, cache: KVCache, num_q_heads: int, k:
 
 
 def _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes):
-    import torch
     cache._fits(prob, w)
     if cache.v is None:
         _refuse(w, "the cache has no values")
@@ -458,10 +459,10 @@ def _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes):
         _refuse(w, f"q must be {cache.dtype} on {dev}, got {q.dtype} on {q.device}")
     if out.shape != shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         _refuse(w, "out must be contiguous, of q's shape, dtype and device")
-    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or lse.device != dev
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != _float32 or lse.device != dev
                             or not lse.is_contiguous()):
         _refuse(w, f"lse must be contiguous fp32 {tuple(shape[:2])}")
-    if slopes is not None and (slopes.shape != shape[1:2] or slopes.dtype != torch.float32
+    if slopes is not None and (slopes.shape != shape[1:2] or slopes.dtype != _float32
                                or slopes.device != dev or not slopes.is_contiguous()):
         _refuse(w, f"slopes must be contiguous fp32 [{shape[1]}]")
     if ws.device != dev or not ws.is_contiguous():
@@ -490,10 +491,9 @@ def attention_selected(prob: Problem, cache: KVCache, q, idx, out, ws, lse=None,
                        softcap: float = 0.0, slopes=None, stream=None) -> None:
     """Attention of every query over the tokens idx [T, k] that an indexer
     selected for it (entries < 0 are padding)."""
-    import torch
     w = "attention_selected"
     heads, opts, *rest = _attention_args(w, prob, cache, q, out, ws, lse, scale, softcap, slopes)
-    if (idx.dim() != 2 or idx.shape[0] != prob.T or idx.dtype != torch.int32
+    if (idx.dim() != 2 or idx.shape[0] != prob.T or idx.dtype != _int32
             or idx.device != cache.device or not idx.is_contiguous()):
         _refuse(w, f"idx must be contiguous int32 [{prob.T}, k] on the cache's device")
     code = _on(cache, lib.misa_attention_selected, prob.ref, cache.ref, q.data_ptr(), heads, opts,

@@ -10,7 +10,10 @@
 // filled by cp.async (16-byte chunks, so that any page size, stride or
 // selection is read row by row; rows that do not exist are zero-filled, so
 // that nothing a masked place holds reaches a product).  The groups' partial
-// rows are joined in shared memory, the chunks' by combine_kernel.
+// rows are joined in shared memory.  Up to eight chunks of a row tile are a
+// cluster, which joins them over distributed shared memory, with what the
+// shared prefix's launch left for the row, and writes the result; more chunks
+// leave partial rows in the workspace for combine_kernel.
 #include "attend.cuh"
 
 #include <algorithm>
@@ -42,8 +45,12 @@ struct Shape {
   static constexpr int big = ring > merge ? ring : merge;
   // q | ring (later the groups' partial rows) | key positions | stage flags | row positions | m, l | scan
   static constexpr int bytes = q_bytes + big + groups * kStages * KB * 4 + groups * kStages * 4 * WM + rows * 4 +
-                               groups * rows * 8 + (kScan + 1 + kScan / 32) * 4 + 16 + 64;
+                               groups * rows * 8 + rows * 4 + (kScan + 1 + kScan / 32) * 4 + 16 + 64;
 };
+
+constexpr int resident_blocks(int bytes) {
+  return bytes <= 0 ? 1 : std::max(1, std::min(8, 227 * 1024 / (bytes + 1024)));
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -75,6 +82,43 @@ __device__ __forceinline__ void group_sync(int group) {
   }
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Reads of block `rank`'s shared memory; without a cluster the block's own.
+__device__ __forceinline__ uint32_t cluster_at(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_at(addr, rank)));
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(cluster_at(addr, rank)));
+  return x;
+}
+
+// Row r of an item among all [T, Hq].
+__device__ __forceinline__ int64_t row_of_item(const AttendArgs& a, const Item& it, int r) {
+  const int g = it.r0 + r;
+  return (int64_t)(it.qb + g / a.G) * a.Hq + it.h * a.G + g % a.G;
+}
+
+template <typename E>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8], E tag) {
+  return make_uint4(pack2(x[0], x[1], tag), pack2(x[2], x[3], tag), pack2(x[4], x[5], tag), pack2(x[6], x[7], tag));
+}
+
 // MODE: which keys; KIND: what is done to the products (Change).
 template <typename E, int D, int WM, int KB, int MODE, int KIND>
 __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
@@ -89,7 +133,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   int* s_mask = s_key + Sh::groups * kStages * KB;
   int* s_pos = s_mask + Sh::groups * kStages * WM;
   float* s_ml = reinterpret_cast<float*>(s_pos + Sh::rows);
-  int* s_sum = reinterpret_cast<int*>(s_ml + Sh::groups * Sh::rows * 2);
+  float* s_lse = s_ml + Sh::groups * Sh::rows * 2;
+  int* s_sum = reinterpret_cast<int*>(s_lse + Sh::rows);
 
   volatile int* s_cut = s_sum + kScan + 1 + kScan / 32;  // something was cut out of a value block
 
@@ -103,7 +148,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   } else {
     total = count_items<MODE>(a, Sh::rows, s_sum);
   }
-  for (int64_t w = blockIdx.x; w < (int64_t)total * a.Hkv; w += gridDim.x) {
+  const int rank = a.cl > 1 ? (int)cluster_rank() : 0;
+  for (int64_t w = blockIdx.x / a.cl; w < (int64_t)total * a.Hkv; w += gridDim.x / a.cl) {
     Item it;
     it.h = (int)(w % a.Hkv);
     if constexpr (MODE == kSelected) {
@@ -147,8 +193,14 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     far = __reduce_max_sync(0xffffffffu, far);
     near = __reduce_min_sync(0xffffffffu, near);
     least = __reduce_min_sync(0xffffffffu, least);
-    const int k1 = MODE == kSelected ? it.k1 : min(it.k1, far + 1);
-    const int nblk = k1 > it.k0 ? (k1 - it.k0 + KB - 1) / KB : 0;
+    // this block's keys: the item's, or its part of the cluster's
+    int k0 = it.k0, k1 = MODE == kSelected ? it.k1 : min(it.k1, far + 1);
+    if (a.cl > 1) {
+      const int per = ((k1 - k0 + a.cl - 1) / a.cl + KB - 1) / KB * KB;
+      k0 += rank * per;
+      k1 = min(k1, k0 + per);
+    }
+    const int nblk = k1 > k0 ? (k1 - k0 + KB - 1) / KB : 0;
     const int mine = nblk > grp ? (nblk - grp + Sh::groups - 1) / Sh::groups : 0;  // blocks of this group
 
     uint32_t fq[D / 16][4];
@@ -169,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     // Lane l knows key l of a block: its position and where its row is.
     const int64_t head = it.h * a.c.head_stride;
     auto key_of = [&](int i) -> int {  // position of this lane's key in the group's i-th block, -1: none
-      const int j = it.k0 + (grp + i * Sh::groups) * KB + lane;
+      const int j = k0 + (grp + i * Sh::groups) * KB + lane;
       if (i >= mine || lane >= KB || j >= k1) return -1;
       if constexpr (MODE == kSelected) return __ldg(a.idx + (int64_t)it.qb * a.k + j);
       return j;
@@ -410,23 +462,67 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = l == 0.f ? 0.f : acc[j] * inv;
       if (MODE != kSelected && *s_cut && least < s_pos[r])
-        poison<E, 8>(a, it.seq, it.h, c * 8, max(it.k0, least + 1), min(k1 - 1, s_pos[r]), acc);
-      const int gr = it.r0 + r;
-      const int64_t row = (int64_t)(it.qb + gr / a.G) * a.Hq + it.h * a.G + gr % a.G;
+        poison<E, 8>(a, it.seq, it.h, c * 8, max(k0, least + 1), min(k1 - 1, s_pos[r]), acc);
+      if (a.cl > 1 || a.finish) {
+        // this block's row, in the place of its first group's
+        float4* d = reinterpret_cast<float4*>(s_o + r * (D + 4) + c * 8);
+        d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (c == 0) s_lse[r] = lse2;
+        continue;
+      }
+      const int64_t row = row_of_item(a, it, r);
       if (a.part_o) {
         float4* d = reinterpret_cast<float4*>(a.part_o + (row * a.nslots + it.slot) * D + c * 8);
         d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (c == 0) a.part_lse[row * a.nslots + it.slot] = lse2;
       } else {
-        uint4 y;
-        y.x = pack2(acc[0], acc[1], tag);
-        y.y = pack2(acc[2], acc[3], tag);
-        y.z = pack2(acc[4], acc[5], tag);
-        y.w = pack2(acc[6], acc[7], tag);
-        *reinterpret_cast<uint4*>(a.out + row * D + c * 8) = y;
+        *reinterpret_cast<uint4*>(a.out + row * D + c * 8) = pack8(acc, tag);
         if (c == 0 && a.lse) a.lse[row] = lse2 * kLn2;
       }
+    }
+    if (a.cl > 1 || a.finish) {
+      // Join the blocks, and the shared prefix's chunks; the rows are spread over the cluster.
+      if (a.cl > 1) cluster_sync();
+      else __syncthreads();
+      const int n_shared = MODE == kOwn && a.finish ? shared_slots(a, it.seq) : 0;
+      for (int i = rank * kThreads + threadIdx.x; i < it.nrows * kChunks; i += a.cl * kThreads) {
+        const int r = i / kChunks, c = i % kChunks;
+        const int64_t row = row_of_item(a, it, r);
+        const uint32_t lse_at = smem_u32(s_lse + r), o_at = smem_u32(s_o + r * (D + 4) + c * 8);
+        const float* pl = a.part_lse + row * a.nslots;
+        float m = -INFINITY;
+        for (int b = 0; b < a.cl; ++b) m = fmaxf(m, ld_cluster(lse_at, b));
+        for (int b = 0; b < n_shared; ++b) m = fmaxf(m, pl[b]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+        auto take = [&](float lse2, const float4& x, const float4& y) {
+          const float f = ex2(lse2 - ref);
+          l += f;
+          acc[0] = fmaf(f, x.x, acc[0]);
+          acc[1] = fmaf(f, x.y, acc[1]);
+          acc[2] = fmaf(f, x.z, acc[2]);
+          acc[3] = fmaf(f, x.w, acc[3]);
+          acc[4] = fmaf(f, y.x, acc[4]);
+          acc[5] = fmaf(f, y.y, acc[5]);
+          acc[6] = fmaf(f, y.z, acc[6]);
+          acc[7] = fmaf(f, y.w, acc[7]);
+        };
+#pragma unroll 4
+        for (int b = 0; b < a.cl; ++b) take(ld_cluster(lse_at, b), ld_cluster4(o_at, b), ld_cluster4(o_at + 16, b));
+#pragma unroll 4
+        for (int b = 0; b < n_shared; ++b) {
+          const float4* src = reinterpret_cast<const float4*>(a.part_o + (row * a.nslots + b) * D + c * 8);
+          take(pl[b], src[0], src[1]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] *= inv;
+        *reinterpret_cast<uint4*>(a.out + row * D + c * 8) = pack8(acc, tag);
+        if (c == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (ref + lg2(l)) * kLn2;
+      }
+      if (a.cl > 1) cluster_sync();  // nobody reads this block's rows any more
     }
   }
 }
@@ -514,13 +610,16 @@ int launch_rows(const AttendArgs& a, int64_t bound, cudaStream_t st) {
   auto kern = attend_kernel<E, D, WM, KB, MODE, KIND>;
   int rc = set_smem_limit((const void*)kern, Sh::bytes);
   if (rc) return rc;
-  // one wave of resident blocks walks the items
-  const int resident = std::max(1, std::min(8, 227 * 1024 / (Sh::bytes + 1024)));
-  const int64_t wave = (int64_t)num_sms() * resident;
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min(bound, wave));
+  // one wave of resident blocks walks the items; clusters, whose lengths
+  // differ, come in several, so that the hardware evens them out
+  const int resident = resident_blocks(Sh::bytes);
+  const int64_t wave = std::max<int64_t>(1, (int64_t)num_sms() * resident / a.cl * (a.cl > 1 ? 8 : 1));
+  const unsigned grid = (unsigned)(std::max<int64_t>(1, std::min(bound, wave)) * a.cl);
   static const char* const names[] = {"attend", "attend_shared", "attend_selected"};
   ProfScope ps(names[MODE], st);
-  return cuda_fail(launch_pdl(kern, dim3(grid), dim3(kThreads), Sh::bytes, st, a), "attend_kernel");
+  return cuda_fail(a.cl > 1 ? launch_pdl_cluster(kern, dim3(grid), dim3(kThreads), a.cl, Sh::bytes, st, a)
+                            : launch_pdl(kern, dim3(grid), dim3(kThreads), Sh::bytes, st, a),
+                   "attend_kernel");
 }
 
 template <typename E, int D, int WM, int KB, int MODE>
@@ -532,7 +631,8 @@ int launch_kind(const AttendArgs& a, int64_t bound, cudaStream_t st) {
 
 template <typename E, int D, int MODE>
 int launch_width(const AttendArgs& a, int rows, int64_t bound, cudaStream_t st) {
-  if (rows == 16) return launch_kind<E, D, 1, 32, MODE>(a, bound, st);
+  // two blocks an SM: one's start and end behind the other's copies
+  if (rows == 16) return launch_kind<E, D, 1, D == 128 ? 16 : 32, MODE>(a, bound, st);
   if (rows == 32) return launch_kind<E, D, 2, 32, MODE>(a, bound, st);
   return launch_kind<E, D, 4, 32, MODE>(a, bound, st);
 }
@@ -567,11 +667,13 @@ struct Part {
   int rows = 16;       // rows of an item
   int chunk = 1;       // keys of an item
   int nch = 0;         // most items along the keys (0: no launch)
+  int cl = 1;          // blocks of a cluster that share an item's keys
   int64_t bound = 0;   // most items, heads included
 };
 struct Plan {
   Part own, shared;    // own: the selected launch too
   int nslots = 1;
+  bool finish = false;  // the own launch writes the results, with what the shared one left
   bool partial = false;
   size_t o_bytes = 0, lse_bytes = 0;
   size_t bytes() const { return partial ? o_bytes + lse_bytes : 256; }
@@ -613,21 +715,32 @@ void pick_rows(Part& p, int64_t rows, bool grid) {
 
 // Cuts the keys of `units` row tiles (heads included), about `keys` each and
 // at most max_keys, into the number of chunks that ends first: the items fill
-// the GPU's places in whole waves, and an item costs its keys and a fixed part.
-void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys) {
+// the GPU's places in whole waves, and an item costs its keys and a fixed part,
+// more of it where partial rows go through the workspace and a second launch.
+void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys, bool clusters) {
   const int64_t places = num_sms() * (p.tc ? 1 : 2);
-  const int64_t fixed = p.tc ? 512 : 192, least = p.tc ? 256 : 128;
+  const int64_t fixed = p.tc ? 512 : 192, least = p.tc ? 256 : 64, join = p.tc ? 512 : 768;
   units = std::max<int64_t>(1, units);
   keys = std::max<int64_t>(1, std::min(keys, max_keys));
-  const int64_t most = std::min<int64_t>((keys + least - 1) / least, 4 * places / units + 1);
+  const int64_t most = (keys + least - 1) / least;
   int64_t best = 1, best_cost = INT64_MAX;
-  for (int64_t c = 1; c <= most; ++c) {
+  auto consider = [&](int64_t c, bool in_cluster) {
+    if (c < 1 || c > most) return;
     const int64_t waves = (units * c + places - 1) / places;
-    const int64_t cost = waves * ((keys + c - 1) / c + fixed) + (c > 1 ? fixed + 8 * c : 0);
-    if (cost < best_cost) {
-      best = c;
-      best_cost = cost;
-    }
+    const int64_t cost = waves * ((keys + c - 1) / c + fixed) + (c == 1 ? 0 : in_cluster ? 64 : join + 8 * c);
+    if (cost >= best_cost) return;
+    best = c;
+    best_cost = cost;
+    p.cl = in_cluster ? (int)c : 1;
+  };
+  consider(1, false);
+  for (int c = 2; clusters && c <= 8; c *= 2) consider(c, true);
+  for (int w = 1; w <= 8; ++w) consider(places * w / units, false);  // the most that w waves hold
+  consider(most, false);
+  if (p.cl > 1) {
+    p.chunk = 1 << 30;
+    p.nch = 1;
+    return;
   }
   int64_t chunk = best == 1 ? max_keys : (keys + best - 1) / best;
   chunk = (chunk + 31) / 32 * 32;
@@ -645,7 +758,7 @@ Plan make_plan(const misa_problem_t* p, const misa_kv_cache_t* c, int Hq, int k,
   if (k > 0) {
     pick_rows(pl.own, G, grid);
     const int64_t units = T * tiles(G, pl.own.rows) * H;
-    split_keys(pl.own, units, k, k);
+    split_keys(pl.own, units, k, k, !pl.own.tc);
     pl.own.bound = units * pl.own.nch;
   } else {
     const int64_t ng = share ? share->num_groups : 0, longest = ng ? share->max_len : 0;
@@ -653,17 +766,20 @@ Plan make_plan(const misa_problem_t* p, const misa_kv_cache_t* c, int Hq, int k,
     pick_rows(pl.own, per_seq, grid);
     // what the prefixes hold is not read per sequence
     const int64_t keys = std::max<int64_t>(p->total_keys - (S - ng) * longest, p->total_keys / 16) / S + 1;
-    split_keys(pl.own, S * tiles(per_seq, pl.own.rows) * H, keys, p->max_seq_len);
+    split_keys(pl.own, S * tiles(per_seq, pl.own.rows) * H, keys, p->max_seq_len,
+               !pl.own.tc);
     pl.own.bound = (T * G / pl.own.rows + S) * H * pl.own.nch;
     if (ng && longest > 0) {
       const int64_t per_group = tiles(T, ng) * G;
       pick_rows(pl.shared, per_group, grid);
-      split_keys(pl.shared, ng * tiles(per_group, pl.shared.rows) * H, longest, longest);
+      split_keys(pl.shared, ng * tiles(per_group, pl.shared.rows) * H, longest, longest, false);
       pl.shared.bound = (T * G / pl.shared.rows + ng) * H * pl.shared.nch;
     }
   }
-  pl.nslots = pl.own.nch + pl.shared.nch;
-  pl.partial = pl.nslots > 1;
+  // The own launch joins the shared prefix's chunks itself where it has a row's own keys at hand.
+  pl.finish = pl.shared.nch > 0 && pl.own.nch == 1 && !pl.own.tc;
+  pl.nslots = (pl.finish ? 0 : pl.own.nch) + pl.shared.nch;
+  pl.partial = pl.shared.nch > 0 || pl.own.nch > 1;
   pl.o_bytes = up256((size_t)(T * Hq) * pl.nslots * c->head_dim * 4);
   pl.lse_bytes = up256((size_t)(T * Hq) * pl.nslots * 4);
   return pl;
@@ -756,6 +872,7 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   a.k = k;
   a.max_seq_len = p->max_seq_len;
   a.nslots = pl.nslots;
+  a.cl = 1;
   if (share && pl.shared.nch) {
     a.ng = share->num_groups;
     a.max_shared = share->max_len;
@@ -776,9 +893,14 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   a.chunk = pl.own.chunk;
   a.nch_max = pl.own.nch;
   a.slot0 = pl.shared.nch;
+  a.cl = pl.own.cl;
+  a.finish = pl.finish;
+  a.shared_chunk = pl.shared.chunk;
+  a.shared_nch = pl.shared.nch;
+  if (pl.own.cl > 1 && !pl.finish) a.part_o = nullptr;
   rc = k > 0 ? launch_attend<kSelected>(a, c->dtype, c->head_dim, pl.own.tc, pl.own.rows, pl.own.bound, st)
              : launch_attend<kOwn>(a, c->dtype, c->head_dim, pl.own.tc, pl.own.rows, pl.own.bound, st);
-  if (rc || !pl.partial) return rc;
+  if (rc || !pl.partial || pl.finish) return rc;
   CombineArgs ca;
   ca.a = a;
   ca.own_chunk = pl.own.chunk;

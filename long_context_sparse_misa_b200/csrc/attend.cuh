@@ -33,6 +33,9 @@ struct AttendArgs {
   int64_t unit;        // the tensor core kernel's rows: elements between them (divides every stride),
   int page_rows, token_rows, head_rows, map_rows;  // strides in rows, and how many there are
   int box, box_align;  // rows of a box of consecutive ones (0: none), and what its first is a multiple of
+  int cl;              // blocks of a cluster that share an item's keys (warp-level kernel)
+  int finish;          // this launch joins the shared prefix's chunks, in slots 0 .., and writes the results
+  int shared_chunk, shared_nch;
   int slot0, nslots;   // this launch's first slot of a row's partial results; slots of a row
 };
 
@@ -180,6 +183,12 @@ __device__ __forceinline__ int own_chunks(const AttendArgs& a, int s, int chunk,
 }
 __device__ __forceinline__ int shared_chunks(const AttendArgs& a, int g, int chunk, int nch_max) {
   return min(nch_max, (shared_len(a, g) + chunk - 1) / chunk);
+}
+
+// Chunks of the shared prefix that sequence s has partial rows of.
+__device__ __forceinline__ int shared_slots(const AttendArgs& a, int s) {
+  const int g = group_of(a, s);
+  return g < 0 ? 0 : shared_chunks(a, g, a.shared_chunk, a.shared_nch);
 }
 
 // Query rows of group g (its sequences' queries are consecutive).

@@ -7,9 +7,11 @@
 //
 // An item is 16 elements of one head (eight pairs): two 16-byte loads, two
 // 16-byte stores and the pairs' eight cosines and sines, which the heads of a
-// token share through L1.  A thread block takes `tokens` consecutive tokens;
-// its warps first find each token's sequence, position and cache row, then
-// all threads walk the items, with the loads of kUnroll items in flight.
+// token share through L1.  A thread block takes `tokens` consecutive tokens,
+// about one round of kUnroll items a thread.  What an item reads depends on its
+// number alone, so its loads go out first, and the block's warps find each
+// token's sequence, position and cache row (a chain of up to four loads) while
+// they are under way.
 #include "cache.cuh"
 
 namespace misa {
@@ -101,6 +103,7 @@ struct AppendArgs {
   uint32_t* status;
   int64_t k_stride, v_stride, q_stride;
   int S, T, Hq, Hkv, D, rope_rows, rope_dim, interleaved, tokens;
+  uint32_t per_magic;  // ceil(2^32 / items of a token): item number -> token by one multiplication
 };
 
 struct Pair16 {
@@ -133,22 +136,59 @@ __device__ __forceinline__ void turn(Pair16& x, const float4 (&cs)[4], bool inte
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
   pdl_wait_then_release();
   __shared__ int64_t s_row[kAppendTokens];
   __shared__ int s_pos[kAppendTokens];
   const int t0 = blockIdx.x * a.tokens;
   const int nt = min(a.tokens, a.T - t0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kPer = D / 16;  // items of a head
+  const int heads = a.Hq + a.Hkv + (a.v ? a.Hkv : 0);
+  const int per_token = heads * kPer, items = nt * per_token;
+  const int turned = a.rope ? a.rope_dim / 16 : 0;
+  struct Where {
+    int tok, h, ca, cb, pair;  // chunks of eight elements, and the angles' number or -1
+  };
+  auto where = [&](int it) {
+    Where w;
+    w.tok = (int)__umulhi((uint32_t)it, a.per_magic);
+    const int in_token = it - w.tok * per_token, i = in_token % kPer;
+    w.h = in_token / kPer;
+    const int rot = w.h < a.Hq + a.Hkv ? turned : 0;
+    // a pair's two halves, or any two chunks: eight lanes read 128 bytes together
+    w.pair = i < rot ? i : -1;
+    w.ca = i < rot ? i : rot + i;
+    w.cb = i < rot ? i + rot : kPer + i;
+    return w;
+  };
+  Pair16 x[kUnroll];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int it = base + u * kAppendThreads;
+      if (it >= items) continue;
+      const Where w = where(it);
+      const int64_t t = t0 + w.tok;
+      const uint16_t* src = w.h < a.Hq           ? a.q + t * a.q_stride + w.h * D
+                            : w.h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (w.h - a.Hq) * D
+                                                 : a.v + t * a.v_stride + (w.h - a.Hq - a.Hkv) * D;
+      x[u].a = __ldcs(reinterpret_cast<const uint4*>(src) + w.ca);
+      x[u].b = __ldcs(reinterpret_cast<const uint4*>(src) + w.cb);
+    }
+  };
+  load(threadIdx.x);
+
   const int live = __ldg(a.qo + a.S);
   for (int i = warp; i < nt; i += kAppendThreads / 32) {
     const int t = t0 + i;
     int pos = -1;
     int64_t row = -1;
     if (t < live) {
+      const int at = __ldg(a.q_pos + t);
       const int seq = warp_segment(a.qo, a.S, t);
       if (lane == 0) {
-        pos = a.q_pos[t];
+        pos = at;
         const int64_t len = __ldg(a.c.ko + seq + 1) - __ldg(a.c.ko + seq);
         uint32_t bad = 0;
         if (pos < 0 || pos >= len) {
@@ -172,56 +212,32 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
   __syncthreads();
 
-  constexpr int kPer = D / 16;  // items of a head
-  const int heads = a.Hq + a.Hkv + (a.v ? a.Hkv : 0);
-  const int per_token = heads * kPer, items = nt * per_token;
-  const int turned = a.rope ? a.rope_dim / 16 : 0;
   for (int base = threadIdx.x; base < items; base += kUnroll * kAppendThreads) {
-    Pair16 x[kUnroll];
-    uint16_t *to_a[kUnroll], *to_b[kUnroll];
-    int pair[kUnroll], pos[kUnroll];
+    if (base != threadIdx.x) load(base);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int it = base + u * kAppendThreads;
-      to_a[u] = nullptr;
       if (it >= items) continue;
-      const int tok = it / per_token, in_token = it - tok * per_token;
-      const int h = in_token / kPer, i = in_token - h * kPer;
-      pos[u] = s_pos[tok];
-      if (pos[u] < 0) continue;
-      const int t = t0 + tok;
-      const bool is_v = h >= a.Hq + a.Hkv;
-      const uint16_t* src;
-      uint16_t* dst;
-      if (h < a.Hq) {
-        src = a.q + t * a.q_stride + h * D;
-        dst = a.q_out + ((int64_t)t * a.Hq + h) * D;
-      } else {
-        const int kh = h - a.Hq - (is_v ? a.Hkv : 0);
-        src = is_v ? a.v + t * a.v_stride + kh * D : a.k + t * a.k_stride + kh * D;
-        dst = (is_v ? a.c.v : a.c.k) + s_row[tok] + kh * a.c.head_stride;
-      }
-      // chunks of eight elements: a pair's two halves, or two neighbours
-      const bool rot = !is_v && i < turned;
-      pair[u] = rot ? i : -1;
-      const bool split = rot && !a.interleaved;
-      const int ca = split ? i : 2 * i, cb = split ? i + turned : 2 * i + 1;
-      x[u].a = __ldcs(reinterpret_cast<const uint4*>(src) + ca);
-      x[u].b = __ldcs(reinterpret_cast<const uint4*>(src) + cb);
-      to_a[u] = dst + ca * 8;
-      to_b[u] = dst + cb * 8;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (!to_a[u]) continue;
-      if (pair[u] >= 0) {
-        const float4* c = reinterpret_cast<const float4*>(a.rope + (int64_t)pos[u] * a.rope_dim) + pair[u] * 2;
+      const Where w = where(it);
+      const int pos = s_pos[w.tok];
+      if (pos < 0) continue;
+      if (w.pair >= 0) {
+        const float4* c = reinterpret_cast<const float4*>(a.rope + (int64_t)pos * a.rope_dim);
         const float4* s = c + a.rope_dim / 8;
-        const float4 cs[4] = {__ldg(c), __ldg(c + 1), __ldg(s), __ldg(s + 1)};
+        // chunk a's and chunk b's pairs, or the eight that the two share
+        const int c0 = a.interleaved ? w.ca : 2 * w.ca, c1 = a.interleaved ? w.cb : 2 * w.ca + 1;
+        const float4 cs[4] = {__ldg(c + c0), __ldg(c + c1), __ldg(s + c0), __ldg(s + c1)};
         turn<E>(x[u], cs, a.interleaved != 0);
       }
-      *reinterpret_cast<uint4*>(to_a[u]) = x[u].a;
-      *reinterpret_cast<uint4*>(to_b[u]) = x[u].b;
+      uint16_t* dst;
+      if (w.h < a.Hq) {
+        dst = a.q_out + ((int64_t)(t0 + w.tok) * a.Hq + w.h) * D;
+      } else {
+        const bool is_v = w.h >= a.Hq + a.Hkv;
+        dst = (is_v ? a.c.v : a.c.k) + s_row[w.tok] + (w.h - a.Hq - (is_v ? a.Hkv : 0)) * a.c.head_stride;
+      }
+      *reinterpret_cast<uint4*>(dst + w.ca * 8) = x[u].a;
+      *reinterpret_cast<uint4*>(dst + w.cb * 8) = x[u].b;
     }
   }
 }
@@ -309,6 +325,7 @@ extern "C" int misa_cache_append(const misa_problem_t* p, const misa_kv_cache_t*
   int tokens = max(1, min(kAppendTokens, kUnroll * kAppendThreads / per_token));
   tokens = max(1, min(tokens, a.T / (2 * num_sms())));
   a.tokens = tokens;
+  a.per_magic = (uint32_t)(((uint64_t(1) << 32) + per_token - 1) / per_token);  // items * per_token < 2^32
   const int blocks = (a.T + tokens - 1) / tokens;
   ProfScope ps("cache_append", static_cast<cudaStream_t>(stream));
   return cuda_fail(cache->dtype == MISA_BF16
