@@ -95,15 +95,23 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32],"
       " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"f"(r[0]),
+      "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]),
+      "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]),
+      "f"(r[26]), "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16],"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -112,7 +120,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 struct Span {
   Item it;
   int k0, k1, n;  // keys, and tiles of them
-  int cut;        // the first tile that holds keys which not all rows see
+  int cut;        // tiles before this one hold keys which not all rows see
   int near;       // every row that sees anything sees the keys up to this one
   bool live;
 };
@@ -151,9 +159,17 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const int* sums, in
     if constexpr (MODE == kOwn) s.k1 = min(s.k1, __reduce_max_sync(0xffffffffu, far) + 1);
   }
   s.n = s.live && s.k1 > s.it.k0 ? (s.k1 - s.k0 + kTile - 1) / kTile : 0;
-  s.cut = s.n;
-  if (MODE != kSelected && s.near < s.k1 - 1) s.cut = s.near < s.k0 ? 0 : min(s.n, (s.near + 1 - s.k0) / kTile);
+  s.cut = 0;
+  if (MODE != kSelected && s.near < s.k1 - 1) s.cut = s.n - (s.near < s.k0 ? 0 : min(s.n, (s.near + 1 - s.k0) / kTile));
   return s;
+}
+
+// First key of tile t.  Contiguous keys come last first: with a bias that falls
+// with the distance the row's maximum is then near its end at once, and no
+// later tile makes it grow (a rescaling of O costs a tile half its softmax).
+template <int MODE>
+__device__ __forceinline__ int tile_start(const Span& s, int t) {
+  return s.k0 + (MODE == kSelected ? t : s.n - 1 - t) * kTile;
 }
 
 // Order of the ring: `lead` key tiles, then value tile t and key tile t + lead
@@ -286,7 +302,6 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int x = warp >> 2;                     // stream
     const int r = ((warp & 3) << 5) + lane;      // row of the stream: its TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -302,6 +317,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       seen += s.n;
       const int rr = (PAIR ? x * kTile : 0) + r;  // row of the item
       const bool real = rr < s.it.nrows;
+      const bool idle = rr - lane >= s.it.nrows;  // no row of this warp is
       const int g = s.it.r0 + (real ? rr : 0);
       const int t = s.it.qb + g / a.G, h = s.it.h * a.G + g % a.G;
       int pos = 0x7ffffffe;
@@ -348,79 +364,76 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       const uint64_t sc2 = pair(sc, sc);
       for (int i = 0; i < mine; ++i) {
         const int tile = PAIR ? i : 2 * i + x;
-        const int base = s.k0 + tile * kTile;
+        const int base = tile_start<MODE>(s, tile);
         if (!warp_wait(&s_full[x], n_s & 1, abort, a.status)) { ok = false; break; }
         ++n_s;
-        tc_fence_after();
-        float v[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, v[q]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) reg_fence32(v[q]);
-        // what this row does not see gets `value`
-        const int last = lim - base;  // contiguous keys: columns up to this one are seen
-        const uint4 inv = *reinterpret_cast<const uint4*>(s_inv + ((first_tile + tile) % kKeep) * 4);
-        auto mask = [&](float value) {
-          if (MODE != kSelected && base + kTile - 1 > least) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (q * 32 + j > last) v[q][j] = value;
-          }
-          if (inv.x | inv.y | inv.z | inv.w) {
-            const uint32_t word[4] = {inv.x, inv.y, inv.z, inv.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (word[q] >> j & 1u) v[q][j] = value;
-          }
-        };
-        if constexpr (KIND == kCapped) {
-          mask(0.f);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) cap4(v[q][j], v[q][j + 1], v[q][j + 2], v[q][j + 3], a);
+        if (idle) {  // what these rows of S hold as P reaches no other row
+          if (lane < 2) mbar_arrive(&p_full[2 * x + lane]);
+          continue;
         }
-        if (bias) {
-          const uint64_t mul = KIND == kCapped ? pair(1.f, 1.f) : pair(a.scale2, a.scale2);
-          const float* far = s_far + ((first_tile + tile) % kKeep) * kTile;
-          const float first = -slope * (float)(pos - base);
-          const uint64_t step = pair(2.f * slope, 2.f * slope), minus = pair(-slope, -slope);
+        tc_fence_after();
+        const int last = lim - base;  // contiguous keys: columns up to this one are seen
+        const int keep = (first_tile + tile) % kKeep;
+        const uint4 inv = *reinterpret_cast<const uint4*>(s_inv + keep * 4);
+        const bool masked = (MODE != kSelected && base + kTile - 1 > least) || (inv.x | inv.y | inv.z | inv.w);
+        // What is done to the products, in place and back to S where it is not nothing, and the
+        // maximum; 32 columns at a time, the next ones' load under way.
+        float v[2][32];
+        float top = -INFINITY;
+        tmem_ld32(tS, v[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
+          float (&u)[32] = v[q & 1];
+          tmem_wait_ld();
+          reg_fence32(u);
+          if (q < 3) tmem_ld32(tS + (q + 1) * 32, v[(q + 1) & 1]);
+          auto mask = [&](float value) {  // what this row does not see gets `value`
+            if (!masked) return;
+            const uint32_t word = q == 0 ? inv.x : q == 1 ? inv.y : q == 2 ? inv.z : inv.w;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if ((MODE != kSelected && q * 32 + j > last) || (word >> j & 1u)) u[j] = value;
+          };
+          if constexpr (KIND == kCapped) {
+            mask(0.f);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) cap4(u[j], u[j + 1], u[j + 2], u[j + 3], a);
+          }
+          if (bias) {
+            const uint64_t mul = KIND == kCapped ? pair(1.f, 1.f) : pair(a.scale2, a.scale2);
+            const float* far = s_far + keep * kTile + q * 32;
+            const float first = -slope * (float)(pos - base);
+            const uint64_t step = pair(2.f * slope, 2.f * slope), minus = pair(-slope, -slope);
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               // slope times the distance: for contiguous keys three steps from an exact start
               uint64_t b[4];
               if constexpr (MODE == kSelected) {
-                const float4 d = *reinterpret_cast<const float4*>(far + q * 32 + j);
-                const float4 e = *reinterpret_cast<const float4*>(far + q * 32 + j + 4);
+                const float4 d = *reinterpret_cast<const float4*>(far + j);
+                const float4 e = *reinterpret_cast<const float4*>(far + j + 4);
                 b[0] = mul2(minus, pair(d.x, d.y)), b[1] = mul2(minus, pair(d.z, d.w));
                 b[2] = mul2(minus, pair(e.x, e.y)), b[3] = mul2(minus, pair(e.z, e.w));
               } else {
                 b[0] = pair(fmaf(slope, (float)(q * 32 + j), first), fmaf(slope, (float)(q * 32 + j + 1), first));
 #pragma unroll
-                for (int u = 1; u < 4; ++u) b[u] = add2(b[u - 1], step);
+                for (int i = 1; i < 4; ++i) b[i] = add2(b[i - 1], step);
               }
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                unpair(fma2(pair(v[q][j + 2 * u], v[q][j + 2 * u + 1]), mul, b[u]), v[q][j + 2 * u], v[q][j + 2 * u + 1]);
+              for (int i = 0; i < 4; ++i)
+                unpair(fma2(pair(u[j + 2 * i], u[j + 2 * i + 1]), mul, b[i]), u[j + 2 * i], u[j + 2 * i + 1]);
             }
-        }
-        mask(-INFINITY);
-        float top4[4];
+          }
+          mask(-INFINITY);
+          float t0 = u[0], t1 = u[1];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          top4[q] = v[q][0];
-#pragma unroll
-          for (int j = 1; j < 31; j += 2) top4[q] = max3(top4[q], v[q][j], v[q][j + 1]);
-          top4[q] = max3(top4[q], v[q][31], v[q][31]);
+          for (int j = 2; j < 30; j += 4) {
+            t0 = max3(t0, u[j], u[j + 1]);
+            t1 = max3(t1, u[j + 2], u[j + 3]);
+          }
+          top = max3(top, max3(t0, u[30], u[31]), t1);
+          if (KIND != kScaled || masked) tmem_st32(tS + q * 32, u);
         }
-        float top = max3(max3(top4[0], top4[1], top4[2]), top4[3], top4[3]);
+        if (KIND != kScaled || masked) tmem_wait_st();
         top *= sc;  // sc > 0: -inf stays
         // an infinite or undefined exponent makes the row's results undefined
         if (!(top < INFINITY)) top = __int_as_float(0x7fffffff);
@@ -433,24 +446,28 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float o[32];
-              uint32_t u[32];
               tmem_ld32(tO + q * 32, o);
               tmem_wait_ld();
               reg_fence32(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * f);
-              tmem_st32(tO + q * 32, u);
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st32(tO + q * 32, o);
             }
           }
         }
         const float minus = ref == -INFINITY ? 0.f : -ref;
         const uint64_t minus2 = pair(minus, minus);
+        tmem_ld32(tS, v[0]);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t p[32];
+        for (int q = 0; q < 4; ++q) {
+          const float (&u)[32] = v[q & 1];
+          tmem_wait_ld();
+          reg_fence32(v[q & 1]);
+          if (q < 3) tmem_ld32(tS + (q + 1) * 32, v[(q + 1) & 1]);
+          uint32_t p[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            uint64_t e = pair(v[2 * q + (j >> 4)][(j & 15) * 2], v[2 * q + (j >> 4)][(j & 15) * 2 + 1]);
+          for (int j = 0; j < 16; ++j) {
+            uint64_t e = pair(u[2 * j], u[2 * j + 1]);
             float e0, e1;
             e = KIND == kScaled ? fma2(e, sc2, minus2) : add2(e, minus2);
             if (poly_pair<KIND>(j)) {
@@ -466,11 +483,13 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
             // the weights' one rounding to the cache's type; their sum keeps fp32
             p[j] = pack2(e0, e1, tag);
           }
-          tmem_st32(tS + q * 32, p);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * x + q]);  // half of the keys
+          tmem_st16(tS + q * 16, p);
+          if (q & 1) {  // half of the keys
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * x + (q >> 1)]);
+          }
         }
       }
       if (!ok) break;
@@ -517,7 +536,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       const bool cut = MODE != kSelected && s.n > 0 && real && cut0 <= lim && *s_cut;
       const bool any_a = PAIR ? mine > 0 : s.n > 0, any_b = !PAIR && s.n > 1;
 #pragma unroll 1
-      for (int q = 0; q < kCols / 32; ++q) {
+      for (int q = 0; q < kCols / 32 && !idle; ++q) {
         float o[32];
         if (any_a) {
           tmem_ld32(ta + q * 32, o);
@@ -558,7 +577,6 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       tc_fence_before();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 9) {
       // ---------------------------------------------------------- finding rows
       // lane l finds keys 4 l .. 4 l + 3 of a tile
@@ -573,7 +591,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         const int32_t* list = a.idx + (int64_t)s.it.qb * a.k;
         const int32_t* table = a.c.table + s.it.seq * a.c.table_stride;
         auto keys_of = [&](int t, int (&key)[4]) {
-          const int j = s.k0 + t * kTile + lane * 4;
+          const int j = tile_start<MODE>(s, t) + lane * 4;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             key[i] = -1;
@@ -606,6 +624,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         pages_of(key, page, off);
         keys_of(1, next);
         for (int t = 0; t < s.n; ++t) {
+          const int start = tile_start<MODE>(s, t);
           int row[4];
           uint32_t bad = 0, none = 0;
 #pragma unroll
@@ -616,7 +635,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
             if (key[i] >= 0 && !there) bad |= ahead ? MISA_STATUS_BAD_INPUT : MISA_STATUS_BOUNDS;
             row[i] = there ? head + r : a.map_rows;  // out of the map's bounds: zeros
             // keys that do not exist; those behind k1 of contiguous ones are told by their number alone
-            if (!there && (MODE == kSelected || s.k0 + t * kTile + lane * 4 + i < s.k1)) none |= 1u << i;
+            if (!there && (MODE == kSelected || start + lane * 4 + i < s.k1)) none |= 1u << i;
           }
           if (bad) set_status(a.status, bad);
           uint32_t word = 0;
@@ -627,7 +646,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
             word |= __shfl_xor_sync(0xffffffffu, word, 2);
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
           }
-          const bool boxed = MODE != kSelected && a.box > 0 && whole && s.k0 + (t + 1) * kTile <= s.k1;
+          const bool boxed = MODE != kSelected && a.box > 0 && whole && start + kTile <= s.k1;
           const float4 far = make_float4(pos - key[0], pos - key[1], pos - key[2], pos - key[3]);
           const int2 place = a.c.table ? make_int2(off[0], page[0]) : make_int2((int)first_row + key[0], 0);
           // the loads of the tiles to come run while this one waits
@@ -759,7 +778,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
           // value tile t, looked over if not all rows see it
           auto take_v = [&](int t) -> int {
             const int v = take();
-            if (v < 0 || MODE == kSelected || t < s.cut) return v;
+            if (v < 0 || t >= s.cut) return v;
             mbar_arrive(cut_ask);
             if (!mbar_wait(cut_done, n_cut++ & 1, abort, a.status)) return -1;
             return v;
@@ -812,13 +831,13 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       bool ok = true;
       for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
         const Span s = span_of<MODE, kRows>(a, s_sum, w);
-        for (int t = s.cut; ok && t < s.n; ++t) {
+        for (int t = 0; ok && t < s.cut; ++t) {
           const int i = cnt + place_v<PAIR>(t, s.n);
           ok = warp_wait(cut_ask, n_cut++ & 1, abort, a.status) &&
                warp_wait(&full[i % kSlots], (i / kSlots) & 1, abort, a.status);
           if (!ok) break;
           uint8_t* tile = ring + (i % kSlots) * L::tile;
-          const int from = s.near + 1 - (s.k0 + t * kTile);  // rows of the tile from here on
+          const int from = s.near + 1 - tile_start<MODE>(s, t);  // rows of the tile from here on
           bool cut = false;
           for (int r = max(from, 0); r < kTile; ++r) {
             // a row's chunks lie in its 128 bytes of each half, in some order
@@ -848,17 +867,6 @@ int launch_tc_one(const AttendArgs& a, const TcMaps& maps, int64_t bound, cudaSt
   auto kern = attend_tc_kernel<E, D, MODE, PAIR, KIND>;
   int rc = set_smem_limit((const void*)kern, L::bytes);
   if (rc) return rc;
-  // The roles' register counts add up to what a block of 128-register threads
-  // is launched with (128 x (192 + 192 + 64 + 64) = 512 x 128); a build that used
-  // fewer would wait for registers for good.
-  static const int regs = [&] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
-  }();
-  if (regs != 128) {
-    set_error("attend_tc: built with %d registers a thread, needs 128", regs);
-    return MISA_ERR_CUDA;
-  }
   const int64_t sms = num_sms();
   const unsigned grid = (unsigned)(bound < 1 ? 1 : bound < sms ? bound : sms);
   static const char* const names[] = {"attend_tc", "attend_tc_shared", "attend_tc_selected"};
