@@ -93,30 +93,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-// 2^x of a pair on the multiply-add pipe, for a share of the exponentials
-// where the special-function pipe (16 a cycle and SM) would bound the softmax.
-// 2^x = 2^n 2^r, n the nearest integer, r in [-1/2, 1/2]; 2^r = 1 + r q(r) with
-// q the polynomial of degree 4 whose largest relative error is least (2^-23.3,
-// found by weighted least squares; 2^-22.3 as evaluated).  x <= 127.  Below
-// -127 (and at -infinity) the result is exactly 0; a NaN is not kept.
-__device__ __forceinline__ uint64_t ex2_poly(uint64_t x) {
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
-  float x0, x1, t0, t1, p0, p1;
-  unpair(x, x0, x1);
-  x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-  const uint64_t t = add2(x, pair(kRound, kRound));
-  const uint64_t r = fma2(add2(t, pair(-kRound, -kRound)), pair(-1.f, -1.f), x);
-  uint64_t p = fma2(pair(0x1.5bba14p-10f, 0x1.5bba14p-10f), r, pair(0x1.3cea88p-7f, 0x1.3cea88p-7f));
-  p = fma2(p, r, pair(0x1.c6b752p-5f, 0x1.c6b752p-5f));
-  p = fma2(p, r, pair(0x1.ebf9bcp-3f, 0x1.ebf9bcp-3f));
-  p = fma2(p, r, pair(0x1.62e42ap-1f, 0x1.62e42ap-1f));
-  p = fma2(p, r, pair(1.f, 1.f));
-  unpair(t, t0, t1);
-  unpair(p, p0, p1);
-  return pair(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
-              __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23)));
-}
-
 __device__ __forceinline__ float min_nan(float x, float y) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));

@@ -27,6 +27,7 @@
 // TB/s from L2 by four threads an SM, 17.9 by six).  Warp 14 looks over value
 // tiles that only some rows see (cut_infinite).  Blocks are persistent, and the
 // fetching warps run ahead into the next item.
+#include <algorithm>
 #include <type_traits>
 
 #include "attend.cuh"
@@ -59,12 +60,6 @@ struct Tc {
   static constexpr int bytes = off_sum + 16 + (kScan + 1 + kScan / 32) * 4 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of a block");
 };
-
-// Which pairs of exponentials are computed by ex2_poly.
-template <int KIND>
-__host__ __device__ constexpr bool poly_pair(int j) {
-  return KIND == kCapped && j % 2 == 1;
-}
 
 template <typename E>
 __host__ __device__ constexpr uint32_t tc_idesc(int N, bool b_mn) {
@@ -335,11 +330,6 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         uint4 v[kC];
 #pragma unroll
         for (int i = 0; i < kC; ++i) v[i] = real ? __ldg(src + c0 + i) : make_uint4(0, 0, 0, 0);
-        if (KIND == kScaled && a.scale2 < 0.f) {  // the softmax works with a positive scale
-#pragma unroll
-          for (int i = 0; i < kC; ++i)
-            v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
-        }
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
           const int c = c0 + i;
@@ -352,9 +342,8 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       }
       float slope = 0.f;
       const bool bias = KIND == kBiased || (KIND == kCapped && a.slopes);
-      if (bias) slope = __ldg(a.slopes + h) * kLog2e;
-      // at least 1e-30, so that a scale of 0 keeps a masked -inf what it is
-      const float sc = KIND == kScaled ? fmaxf(fabsf(a.scale2), 1e-30f) : 1.f;
+      if (a.slopes && bias) slope = __ldg(a.slopes + h) * kLog2e;
+      const float sc = KIND == kScaled ? a.scale2 : 1.f;
       // contiguous keys: the last one that this row sees
       const int lim = MODE == kSelected ? 0x7fffffff : min(pos, s.k1 - 1);
       const int least = __reduce_min_sync(0xffffffffu, lim);
@@ -372,27 +361,22 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
           continue;
         }
         tc_fence_after();
+        float v[2][32];
+        tmem_ld32(tS, v[0]);
         const int last = lim - base;  // contiguous keys: columns up to this one are seen
         const int keep = (first_tile + tile) % kKeep;
         const uint4 inv = *reinterpret_cast<const uint4*>(s_inv + keep * 4);
         const bool masked = (MODE != kSelected && base + kTile - 1 > least) || (inv.x | inv.y | inv.z | inv.w);
         // What is done to the products, in place and back to S where it is not nothing, and the
         // maximum; 32 columns at a time, the next ones' load under way.
-        float v[2][32];
         float top = -INFINITY;
-        tmem_ld32(tS, v[0]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float (&u)[32] = v[q & 1];
-          tmem_wait_ld();
-          reg_fence32(u);
-          if (q < 3) tmem_ld32(tS + (q + 1) * 32, v[(q + 1) & 1]);
+        auto piece = [&](int q, float (&u)[32]) {
           auto mask = [&](float value) {  // what this row does not see gets `value`
             if (!masked) return;
             const uint32_t word = q == 0 ? inv.x : q == 1 ? inv.y : q == 2 ? inv.z : inv.w;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if ((MODE != kSelected && q * 32 + j > last) || (word >> j & 1u)) u[j] = value;
+              if ((MODE != kSelected && j > last - q * 32) || (word >> j & 1u)) u[j] = value;
           };
           if constexpr (KIND == kCapped) {
             mask(0.f);
@@ -402,7 +386,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
           if (bias) {
             const uint64_t mul = KIND == kCapped ? pair(1.f, 1.f) : pair(a.scale2, a.scale2);
             const float* far = s_far + keep * kTile + q * 32;
-            const float first = -slope * (float)(pos - base);
+            const float first = -slope * (float)(pos - base - q * 32);
             const uint64_t step = pair(2.f * slope, 2.f * slope), minus = pair(-slope, -slope);
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
@@ -414,7 +398,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
                 b[0] = mul2(minus, pair(d.x, d.y)), b[1] = mul2(minus, pair(d.z, d.w));
                 b[2] = mul2(minus, pair(e.x, e.y)), b[3] = mul2(minus, pair(e.z, e.w));
               } else {
-                b[0] = pair(fmaf(slope, (float)(q * 32 + j), first), fmaf(slope, (float)(q * 32 + j + 1), first));
+                b[0] = pair(fmaf(slope, (float)j, first), fmaf(slope, (float)(j + 1), first));
 #pragma unroll
                 for (int i = 1; i < 4; ++i) b[i] = add2(b[i - 1], step);
               }
@@ -432,6 +416,17 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
           }
           top = max3(top, max3(t0, u[30], u[31]), t1);
           if (KIND != kScaled || masked) tmem_st32(tS + q * 32, u);
+        };
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+          tmem_wait_ld();
+          reg_fence32(v[0]);
+          tmem_ld32(tS + q * 32 + 32, v[1]);
+          piece(q, v[0]);
+          tmem_wait_ld();
+          reg_fence32(v[1]);
+          if (q == 0) tmem_ld32(tS + 64, v[0]);
+          piece(q + 1, v[1]);
         }
         if (KIND != kScaled || masked) tmem_wait_st();
         top *= sc;  // sc > 0: -inf stays
@@ -457,39 +452,38 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         }
         const float minus = ref == -INFINITY ? 0.f : -ref;
         const uint64_t minus2 = pair(minus, minus);
-        tmem_ld32(tS, v[0]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float (&u)[32] = v[q & 1];
-          tmem_wait_ld();
-          reg_fence32(v[q & 1]);
-          if (q < 3) tmem_ld32(tS + (q + 1) * 32, v[(q + 1) & 1]);
+        auto weigh = [&](int q, const float (&u)[32]) {
           uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             uint64_t e = pair(u[2 * j], u[2 * j + 1]);
             float e0, e1;
             e = KIND == kScaled ? fma2(e, sc2, minus2) : add2(e, minus2);
-            if (poly_pair<KIND>(j)) {
-              e = ex2_poly(e);
-              unpair(e, e0, e1);
-            } else {
-              unpair(e, e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              e = pair(e0, e1);
-            }
+            unpair(e, e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            e = pair(e0, e1);
             l01 = add2(l01, e);
             // the weights' one rounding to the cache's type; their sum keeps fp32
             p[j] = pack2(e0, e1, tag);
           }
           tmem_st16(tS + q * 16, p);
-          if (q & 1) {  // half of the keys
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * x + (q >> 1)]);
-          }
+        };
+        tmem_ld32(tS, v[0]);
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+          tmem_wait_ld();
+          reg_fence32(v[0]);
+          tmem_ld32(tS + q * 32 + 32, v[1]);
+          weigh(q, v[0]);
+          tmem_wait_ld();
+          reg_fence32(v[1]);
+          if (q == 0) tmem_ld32(tS + 64, v[0]);
+          weigh(q + 1, v[1]);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + (q >> 1)]);  // half of the keys
         }
       }
       if (!ok) break;
@@ -867,8 +861,10 @@ int launch_tc_one(const AttendArgs& a, const TcMaps& maps, int64_t bound, cudaSt
   auto kern = attend_tc_kernel<E, D, MODE, PAIR, KIND>;
   int rc = set_smem_limit((const void*)kern, L::bytes);
   if (rc) return rc;
-  const int64_t sms = num_sms();
-  const unsigned grid = (unsigned)(bound < 1 ? 1 : bound < sms ? bound : sms);
+  // A selection's items are short and alike: one block an SM walks them.  Others are long, and their
+  // lengths differ: a block each, which the hardware hands out (2 x 1000 queries: 563 -> 514 us).
+  const int64_t most = MODE == kSelected ? num_sms() : 0x7fffffff;
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min(bound, most));
   static const char* const names[] = {"attend_tc", "attend_tc_shared", "attend_tc_selected"};
   ProfScope ps(names[MODE], st);
   return cuda_fail(launch_pdl(kern, dim3(grid), dim3(kTcThreads), L::bytes, st, a, maps),
@@ -877,10 +873,10 @@ int launch_tc_one(const AttendArgs& a, const TcMaps& maps, int64_t bound, cudaSt
 
 template <typename E, int D, int MODE, bool PAIR>
 int launch_tc_kind(const AttendArgs& a, const TcMaps& m, int64_t bound, cudaStream_t st) {
-  // a scale of 0 times a masked -inf: the capped form scales before it masks
-  return a.cap2 > 0.f ? launch_tc_one<E, D, MODE, PAIR, kCapped>(a, m, bound, st)
-         : a.slopes   ? launch_tc_one<E, D, MODE, PAIR, kBiased>(a, m, bound, st)
-                      : launch_tc_one<E, D, MODE, PAIR, kScaled>(a, m, bound, st);
+  // the scaled form takes the maximum before it scales: a scale that is not positive goes to the biased one
+  return a.cap2 > 0.f                         ? launch_tc_one<E, D, MODE, PAIR, kCapped>(a, m, bound, st)
+         : a.slopes || !(a.scale2 > 0.f) ? launch_tc_one<E, D, MODE, PAIR, kBiased>(a, m, bound, st)
+                                              : launch_tc_one<E, D, MODE, PAIR, kScaled>(a, m, bound, st);
 }
 
 template <int MODE, bool PAIR>
