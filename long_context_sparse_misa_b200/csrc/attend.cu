@@ -108,6 +108,14 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
   return x;
 }
 
+// Keys [k0, k1) of an item, or the part of them that block `rank` of its cluster takes.
+__device__ __forceinline__ int2 part_of(const AttendArgs& a, int k0, int k1, int rank, int block) {
+  if (a.cl == 1) return make_int2(k0, k1);
+  const int shift = a.cl == 2 ? 1 : a.cl == 4 ? 2 : 3;
+  const int per = (((max(k1 - k0, 0) + a.cl - 1) >> shift) + block - 1) / block * block;
+  return make_int2(k0 + rank * per, min(k1, k0 + (rank + 1) * per));
+}
+
 // Row r of an item among all [T, Hq].
 __device__ __forceinline__ int64_t row_of_item(const AttendArgs& a, const Item& it, int r) {
   const int g = it.r0 + r;
@@ -142,25 +150,60 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   const int wm = warp % WM, grp = warp / WM;
   const E tag = E();
 
+  const bool few = (MODE == kOwn ? a.S : a.ng) <= 32 && a.blocks == 0;
   int total = 0;
   if constexpr (MODE == kSelected) {
     total = a.T * ((a.G + Sh::rows - 1) / Sh::rows) * a.nch_max;
+  } else if (few) {
+    total = count_few<MODE>(a, Sh::rows);
   } else {
     total = count_items<MODE>(a, Sh::rows, s_sum);
   }
   const int rank = a.cl > 1 ? (int)cluster_rank() : 0;
-  for (int64_t w = blockIdx.x / a.cl; w < (int64_t)total * a.Hkv; w += gridDim.x / a.cl) {
+  int64_t w = blockIdx.x / a.cl, end = (int64_t)total * a.Hkv;
+  Balance bal(a, total);
+  const bool balanced = MODE == kOwn && a.blocks > 0;
+  if (balanced) {
+    w = (int)blockIdx.x < bal.blocks ? bal.begin(blockIdx.x) : 0;
+    end = (int)blockIdx.x < bal.blocks ? bal.begin(blockIdx.x + 1) : 0;
+  }
+  while (w < end) {
     Item it;
-    it.h = (int)(w % a.Hkv);
     if constexpr (MODE == kSelected) {
-      if (!find_selected(a, Sh::rows, (int)(w / a.Hkv), it)) continue;
+      it.h = (int)(w % a.Hkv);
+      const bool live = find_selected(a, Sh::rows, (int)(w / a.Hkv), it);
+      w += gridDim.x / a.cl;
+      if (!live) continue;
+    } else if (balanced) {
+      w += find_balanced(a, bal, Sh::rows, s_sum, w, end, blockIdx.x, it);
     } else {
-      find_item<MODE>(a, Sh::rows, s_sum, (int)(w / a.Hkv), it);
+      it.h = (int)(w % a.Hkv);
+      if (few) find_few<MODE>(a, Sh::rows, (int)(w / a.Hkv), it);
+      else find_item<MODE>(a, Sh::rows, s_sum, (int)(w / a.Hkv), it);
+      w += gridDim.x / a.cl;
     }
     __syncthreads();  // the previous item is done with shared memory
 
+    // A list's first entries are read ahead of everything else: they lead to the pages, those to the rows.
+    int ahead[2] = {-1, -1};
+    if constexpr (MODE == kSelected) {
+      const int2 part = part_of(a, it.k0, it.k1, rank, KB);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = part.x + (grp + i * Sh::groups) * KB + lane;
+        if (lane < KB && j < part.y) ahead[i] = __ldg(a.idx + (int64_t)it.qb * a.k + j);
+      }
+    }
     if (threadIdx.x == 0) *s_cut = 0;
-    // Rows: their queries' positions (-1 sees nothing) and, swizzled, their q.
+    // Rows: their q, swizzled, and their queries' positions (-1 sees nothing).
+    constexpr int kQ = Sh::rows * kChunks / kThreads;
+    uint4 qv[kQ];
+#pragma unroll
+    for (int u = 0; u < kQ; ++u) {
+      const int i = threadIdx.x + u * kThreads, r = i / kChunks;
+      qv[u] = make_uint4(0, 0, 0, 0);
+      if (r < it.nrows) qv[u] = __ldg(reinterpret_cast<const uint4*>(a.q + row_of_item(a, it, r) * D) + i % kChunks);
+    }
     for (int r = threadIdx.x; r < Sh::rows; r += kThreads) {
       int pos = -1;
       if (r < it.nrows) {
@@ -171,15 +214,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       }
       s_pos[r] = pos;
     }
-    for (int i = threadIdx.x; i < Sh::rows * kChunks; i += kThreads) {
-      const int r = i / kChunks, c = i % kChunks;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < it.nrows) {
-        const int g = it.r0 + r;
-        x = __ldg(reinterpret_cast<const uint4*>(
-                      a.q + ((int64_t)(it.qb + g / a.G) * a.Hq + it.h * a.G + g % a.G) * D) + c);
-      }
-      *reinterpret_cast<uint4*>(s_q + r * Sh::row_bytes + ((c ^ (r & 7)) << 4)) = x;
+#pragma unroll
+    for (int u = 0; u < kQ; ++u) {
+      const int i = threadIdx.x + u * kThreads, r = i / kChunks, c = i % kChunks;
+      *reinterpret_cast<uint4*>(s_q + r * Sh::row_bytes + ((c ^ (r & 7)) << 4)) = qv[u];
     }
     __syncthreads();
     // Furthest and nearest position of the real rows; least: of those that see anything.
@@ -194,12 +232,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     near = __reduce_min_sync(0xffffffffu, near);
     least = __reduce_min_sync(0xffffffffu, least);
     // this block's keys: the item's, or its part of the cluster's
-    int k0 = it.k0, k1 = MODE == kSelected ? it.k1 : min(it.k1, far + 1);
-    if (a.cl > 1) {
-      const int per = ((k1 - k0 + a.cl - 1) / a.cl + KB - 1) / KB * KB;
-      k0 += rank * per;
-      k1 = min(k1, k0 + per);
-    }
+    const int2 part = part_of(a, it.k0, MODE == kSelected ? it.k1 : min(it.k1, far + 1), rank, KB);
+    const int k0 = part.x, k1 = part.y;
     const int nblk = k1 > k0 ? (k1 - k0 + KB - 1) / KB : 0;
     const int mine = nblk > grp ? (nblk - grp + Sh::groups - 1) / Sh::groups : 0;  // blocks of this group
 
@@ -273,9 +307,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     // kStages - 1 blocks in flight; positions two blocks ahead of the copies, rows one.
-    int key_a = key_of(0);
+    int key_a = MODE == kSelected ? ahead[0] : key_of(0);
     int64_t row_a = row_of(key_a);
-    int key_b = key_of(1);
+    int key_b = MODE == kSelected ? ahead[1] : key_of(1);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
       const int64_t row_b = row_of(key_b);
@@ -490,15 +524,26 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       for (int i = rank * kThreads + threadIdx.x; i < it.nrows * kChunks; i += a.cl * kThreads) {
         const int r = i / kChunks, c = i % kChunks;
         const int64_t row = row_of_item(a, it, r);
+        // The chunk's lanes share the row: lane b reads block b's weight, and all the chunks at once.
         const uint32_t lse_at = smem_u32(s_lse + r), o_at = smem_u32(s_o + r * (D + 4) + c * 8);
+        const uint32_t team = (kChunks == 16 ? 0xffffu : 0xffu) << (lane & ~(kChunks - 1));
+        float4 ox[8], oy[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          if (b < a.cl) {
+            ox[b] = ld_cluster4(o_at, b);
+            oy[b] = ld_cluster4(o_at + 16, b);
+          }
+        const float mine_lse = c < a.cl ? ld_cluster(lse_at, c) : -INFINITY;
         const float* pl = a.part_lse + row * a.nslots;
-        float m = -INFINITY;
-        for (int b = 0; b < a.cl; ++b) m = fmaxf(m, ld_cluster(lse_at, b));
-        for (int b = 0; b < n_shared; ++b) m = fmaxf(m, pl[b]);
+        float m = mine_lse;
+        for (int b = c; b < n_shared; b += kChunks) m = fmaxf(m, pl[b]);
+#pragma unroll
+        for (int o = kChunks / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(team, m, o));
         const float ref = m == -INFINITY ? 0.f : m;
+        const float mine_f = ex2(mine_lse - ref);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
-        auto take = [&](float lse2, const float4& x, const float4& y) {
-          const float f = ex2(lse2 - ref);
+        auto take = [&](float f, const float4& x, const float4& y) {
           l += f;
           acc[0] = fmaf(f, x.x, acc[0]);
           acc[1] = fmaf(f, x.y, acc[1]);
@@ -509,12 +554,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
           acc[6] = fmaf(f, y.z, acc[6]);
           acc[7] = fmaf(f, y.w, acc[7]);
         };
-#pragma unroll 4
-        for (int b = 0; b < a.cl; ++b) take(ld_cluster(lse_at, b), ld_cluster4(o_at, b), ld_cluster4(o_at + 16, b));
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          if (b < a.cl) take(__shfl_sync(team, mine_f, b, kChunks), ox[b], oy[b]);
 #pragma unroll 4
         for (int b = 0; b < n_shared; ++b) {
           const float4* src = reinterpret_cast<const float4*>(a.part_o + (row * a.nslots + b) * D + c * 8);
-          take(pl[b], src[0], src[1]);
+          take(ex2(pl[b] - ref), src[0], src[1]);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -542,6 +588,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
   const AttendArgs& a = p.a;
   __shared__ float s_o[kWarps][D];
   __shared__ float s_l[kWarps];
+  __shared__ int s_sum[kScan + 1 + kScan / 32];
+  if (a.blocks > 0) count_items<kOwn>(a, a.rows, s_sum);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;
   const int t = (int)(row / a.Hq);
@@ -549,7 +597,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
   int n_own = p.own_max, n_shared = 0;
   if (!p.selected) {
     const int seq = warp_segment(a.qo, a.S, t);
-    n_own = own_chunks(a, seq, p.own_chunk, p.own_max);
+    n_own = a.blocks > 0 ? balanced_slots(a, s_sum, seq, t, (int)(row % a.Hq)) : own_chunks(a, seq, p.own_chunk, p.own_max);
     const int g = group_of(a, seq);
     if (g >= 0) n_shared = shared_chunks(a, g, p.shared_chunk, p.shared_max);
   }
@@ -614,7 +662,7 @@ int launch_rows(const AttendArgs& a, int64_t bound, cudaStream_t st) {
   // differ, come in several, so that the hardware evens them out
   const int resident = resident_blocks(Sh::bytes);
   const int64_t wave = std::max<int64_t>(1, (int64_t)num_sms() * resident / a.cl * (a.cl > 1 ? 8 : 1));
-  const unsigned grid = (unsigned)(std::max<int64_t>(1, std::min(bound, wave)) * a.cl);
+  const unsigned grid = a.blocks > 0 ? (unsigned)a.blocks : (unsigned)(std::max<int64_t>(1, std::min(bound, wave)) * a.cl);
   static const char* const names[] = {"attend", "attend_shared", "attend_selected"};
   ProfScope ps(names[MODE], st);
   return cuda_fail(a.cl > 1 ? launch_pdl_cluster(kern, dim3(grid), dim3(kThreads), a.cl, Sh::bytes, st, a)
@@ -668,6 +716,7 @@ struct Part {
   int chunk = 1;       // keys of an item
   int nch = 0;         // most items along the keys (0: no launch)
   int cl = 1;          // blocks of a cluster that share an item's keys
+  int cuts = 0;        // balanced launch: most_cuts of its blocks (0: not one)
   int64_t bound = 0;   // most items, heads included
 };
 struct Plan {
@@ -714,12 +763,15 @@ void pick_rows(Part& p, int64_t rows, bool grid) {
 }
 
 // Cuts the keys of `units` row tiles (heads included), about `keys` each and
-// at most max_keys, into the number of chunks that ends first: the items fill
-// the GPU's places in whole waves, and an item costs its keys and a fixed part,
-// more of it where partial rows go through the workspace and a second launch.
-void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys, bool clusters) {
+// at most max_keys, so that the launch ends soonest.  Costs are in keys of a
+// block (512 bytes at 23 GB/s, 22 ns, in the warp-level kernel): the items fill
+// the GPU's places in whole waves, and an item costs its keys and a fixed part;
+// a cluster's join little, partial rows through the workspace a second launch
+// (9 us).  Own keys may instead be balanced over all blocks: no waves.
+constexpr int kStep = 128;  // keys of a balanced launch's step
+void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys, bool clusters, bool balance) {
   const int64_t places = num_sms() * (p.tc ? 1 : 2);
-  const int64_t fixed = p.tc ? 512 : 192, least = p.tc ? 256 : 64, join = p.tc ? 512 : 768;
+  const int64_t fixed = p.tc ? 512 : 96, least = p.tc ? 256 : 64, join = p.tc ? 512 : 420;
   units = std::max<int64_t>(1, units);
   keys = std::max<int64_t>(1, std::min(keys, max_keys));
   const int64_t most = (keys + least - 1) / least;
@@ -735,8 +787,18 @@ void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys, bool clu
   };
   consider(1, false);
   for (int c = 2; clusters && c <= 8; c *= 2) consider(c, true);
-  for (int w = 1; w <= 8; ++w) consider(places * w / units, false);  // the most that w waves hold
-  consider(most, false);
+  if (balance) {
+    if ((units * keys + places - 1) / places + (units / places + 2) * fixed + join < best_cost) {
+      p.cl = 1;
+      p.cuts = (int)std::max<int64_t>(8, (2 * places + units - 1) / units);
+      p.chunk = kStep;
+      p.nch = p.cuts + 2;
+      return;
+    }
+  } else {
+    for (int w = 1; w <= 8; ++w) consider(places * w / units, false);  // the most that w waves hold
+    consider(most, false);
+  }
   if (p.cl > 1) {
     p.chunk = 1 << 30;
     p.nch = 1;
@@ -758,21 +820,21 @@ Plan make_plan(const misa_problem_t* p, const misa_kv_cache_t* c, int Hq, int k,
   if (k > 0) {
     pick_rows(pl.own, G, grid);
     const int64_t units = T * tiles(G, pl.own.rows) * H;
-    split_keys(pl.own, units, k, k, !pl.own.tc);
+    split_keys(pl.own, units, k, k, !pl.own.tc, false);
     pl.own.bound = units * pl.own.nch;
   } else {
     const int64_t ng = share ? share->num_groups : 0, longest = ng ? share->max_len : 0;
     const int64_t per_seq = tiles(T, S) * G;
     pick_rows(pl.own, per_seq, grid);
     // what the prefixes hold is not read per sequence
-    const int64_t keys = std::max<int64_t>(p->total_keys - (S - ng) * longest, p->total_keys / 16) / S + 1;
+    const int64_t keys = std::max<int64_t>(p->total_keys - S * longest, p->total_keys / 64) / S + 1;
     split_keys(pl.own, S * tiles(per_seq, pl.own.rows) * H, keys, p->max_seq_len,
-               !pl.own.tc);
+               !pl.own.tc, !pl.own.tc);
     pl.own.bound = (T * G / pl.own.rows + S) * H * pl.own.nch;
     if (ng && longest > 0) {
       const int64_t per_group = tiles(T, ng) * G;
       pick_rows(pl.shared, per_group, grid);
-      split_keys(pl.shared, ng * tiles(per_group, pl.shared.rows) * H, longest, longest, false);
+      split_keys(pl.shared, ng * tiles(per_group, pl.shared.rows) * H, longest, longest, false, false);
       pl.shared.bound = (T * G / pl.shared.rows + ng) * H * pl.shared.nch;
     }
   }
@@ -873,6 +935,7 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   a.max_seq_len = p->max_seq_len;
   a.nslots = pl.nslots;
   a.cl = 1;
+  a.most_cuts = a.most_steps = 1;
   if (share && pl.shared.nch) {
     a.ng = share->num_groups;
     a.max_shared = share->max_len;
@@ -895,6 +958,13 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   a.slot0 = pl.shared.nch;
   a.cl = pl.own.cl;
   a.finish = pl.finish;
+  a.rows = pl.own.rows;
+  if (pl.own.cuts) {
+    a.blocks = num_sms() * 2;
+    a.most_cuts = pl.own.cuts;
+    a.most_steps = (p->max_seq_len + kStep - 1) / kStep;
+    a.nch_max = 1 << 30;
+  }
   a.shared_chunk = pl.shared.chunk;
   a.shared_nch = pl.shared.nch;
   if (pl.own.cl > 1 && !pl.finish) a.part_o = nullptr;

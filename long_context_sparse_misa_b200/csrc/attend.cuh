@@ -36,6 +36,8 @@ struct AttendArgs {
   int cl;              // blocks of a cluster that share an item's keys (warp-level kernel)
   int finish;          // this launch joins the shared prefix's chunks, in slots 0 .., and writes the results
   int shared_chunk, shared_nch;
+  int blocks, most_steps, most_cuts;  // balanced launch (blocks > 0): see Balance
+  int rows;            // rows of an item
   int slot0, nslots;   // this launch's first slot of a row's partial results; slots of a row
 };
 
@@ -154,6 +156,7 @@ __device__ __forceinline__ int prefix_of(const AttendArgs& a, int s) {
 // Items along the keys: own mode at least one (a row that sees nothing is
 // written by it), shared mode none for an empty prefix.
 __device__ __forceinline__ int own_chunks(const AttendArgs& a, int s, int chunk, int nch_max) {
+  if (nch_max == 1) return 1;
   const int own = seq_len(a, s) - prefix_of(a, s);
   return min(nch_max, max(1, (max(own, 0) + chunk - 1) / chunk));
 }
@@ -226,26 +229,30 @@ __device__ __forceinline__ int count_items(const AttendArgs& a, int rows, int* s
   return sums[kScan];
 }
 
-// Item `i` (without the head) of those that count_items counted; every thread
-// finds the same one.
+// The unit of item `i` of those that count_items counted, and the items before it.
 template <int MODE>
-__device__ __forceinline__ void find_item(const AttendArgs& a, int rows, const int* sums, int i, Item& it) {
+__device__ __forceinline__ int find_unit(const AttendArgs& a, int rows, const int* sums, int i, int& before) {
   const int units = MODE == kOwn ? a.S : a.ng;
   const int per = (units + kScan - 1) / kScan;
   int u = upper_segment<int>(sums, kScan, i) * per;
-  i -= sums[u / per];
+  before = sums[u / per];
   for (;; ++u) {
     const int n = unit_items<MODE>(a, u, rows);
-    if (i < n || u + 1 >= units) break;
-    i -= n;
+    if (i - before < n || u + 1 >= units) return u;
+    before += n;
   }
+}
+
+// Item `i` (without the head) of unit u, the items before whose are counted off.
+template <int MODE>
+__device__ __forceinline__ void item_of_unit(const AttendArgs& a, int rows, int u, int i, Item& it) {
   const int2 q = MODE == kOwn ? make_int2(__ldg(a.qo + u), __ldg(a.qo + u + 1)) : group_queries(a, u);
   const int nch = MODE == kOwn ? own_chunks(a, u, a.chunk, a.nch_max)
                                : shared_chunks(a, u, a.chunk, a.nch_max);
   const int all = max(0, min(q.y, a.T) - q.x) * a.G;
   const int tiles = (all + rows - 1) / rows;
   // the last row tiles see the most keys: they start first
-  const int tile = tiles - 1 - i / nch, c = i % nch;
+  const int tile = nch == 1 ? tiles - 1 - i : tiles - 1 - i / nch, c = nch == 1 ? 0 : i % nch;
   it.qb = q.x;
   it.r0 = tile * rows;
   it.nrows = min(rows, all - it.r0);
@@ -255,6 +262,87 @@ __device__ __forceinline__ void find_item(const AttendArgs& a, int rows, const i
   it.seq = MODE == kOwn ? u : __ldg(a.so + u);
   it.k0 = min(hi, lo + c * a.chunk);
   it.k1 = c == nch - 1 ? hi : min(hi, lo + (c + 1) * a.chunk);
+}
+
+// Item `i` (without the head) of those that count_items counted; every thread
+// finds the same one.
+template <int MODE>
+__device__ __forceinline__ void find_item(const AttendArgs& a, int rows, const int* sums, int i, Item& it) {
+  int before;
+  const int u = find_unit<MODE>(a, rows, sums, i, before);
+  item_of_unit<MODE>(a, rows, u, i - before, it);
+}
+
+// The same for up to 32 units, by each warp for itself, without count_items:
+// a launch of a few microseconds spends less on it than on two barriers.
+template <int MODE>
+__device__ __forceinline__ int count_few(const AttendArgs& a, int rows) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < (MODE == kOwn ? a.S : a.ng) ? unit_items<MODE>(a, lane, rows) : 0);
+}
+template <int MODE>
+__device__ __forceinline__ void find_few(const AttendArgs& a, int rows, int i, Item& it) {
+  const int lane = threadIdx.x & 31;
+  const int n = lane < (MODE == kOwn ? a.S : a.ng) ? unit_items<MODE>(a, lane, rows) : 0;
+  int x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  const int u = __popc(__ballot_sync(0xffffffffu, x <= i));  // units that end before item i
+  item_of_unit<MODE>(a, rows, u, i - __shfl_sync(0xffffffffu, x - n, u & 31), it);
+}
+
+// A balanced launch (own mode): the steps of `chunk` keys of all row tiles and
+// heads stand in one line, which the blocks cut into equal parts, so that all
+// end together whatever the lengths.  A part may begin or end inside a row
+// tile's keys, whose partial rows then have a slot for each block that shares
+// them: no more than most_cuts + 2, since a part is at least most_steps /
+// most_cuts long.
+struct Balance {
+  int64_t all;  // steps
+  int blocks;   // that share them
+  __device__ __forceinline__ Balance(const AttendArgs& a, int total) : all((int64_t)total * a.Hkv) {
+    const int64_t most = min(all, all * a.most_cuts / a.most_steps);  // no block without a step
+    blocks = (int)(most < 1 ? 1 : most < a.blocks ? most : a.blocks);
+  }
+  __device__ __forceinline__ int64_t begin(int b) const { return b * all / blocks; }
+  __device__ __forceinline__ int block_of(int64_t step) const { return (int)(((step + 1) * blocks - 1) / all); }
+};
+
+// The item that begins at step `at` and goes to its row tile's end or to step `end`; returns its steps.
+__device__ __forceinline__ int find_balanced(const AttendArgs& a, const Balance& bal, int rows, const int* sums,
+                                             int64_t at, int64_t end, int block, Item& it) {
+  int before;
+  const int u = find_unit<kOwn>(a, rows, sums, (int)(at / a.Hkv), before);
+  const int first = __ldg(a.qo + u), all = max(0, min(__ldg(a.qo + u + 1), a.T) - first) * a.G;
+  const int steps = own_chunks(a, u, a.chunk, a.nch_max);
+  const int rem = (int)(at - (int64_t)before * a.Hkv), k = rem % steps, line = rem / steps;
+  const int tile = line / a.Hkv;
+  it.h = line % a.Hkv;
+  it.seq = u;
+  it.qb = first;
+  it.r0 = tile * rows;
+  it.nrows = min(rows, all - it.r0);
+  const int n = (int)min((int64_t)(steps - k), end - at);
+  const int lo = prefix_of(a, u), hi = seq_len(a, u);
+  it.k0 = min(hi, lo + k * a.chunk);
+  it.k1 = k + n == steps ? hi : min(hi, lo + (k + n) * a.chunk);
+  it.slot = a.slot0 + block - bal.block_of(at - k);
+  return n;
+}
+
+// Partial rows that a balanced launch left for row (t, head hq) of sequence u.
+__device__ __forceinline__ int balanced_slots(const AttendArgs& a, const int* sums, int u, int t, int hq) {
+  const Balance bal(a, sums[kScan]);
+  const int per = (a.S + kScan - 1) / kScan;
+  int before = sums[u / per];
+  for (int v = u / per * per; v < u; ++v) before += unit_items<kOwn>(a, v, a.rows);
+  const int steps = own_chunks(a, u, a.chunk, a.nch_max);
+  const int tile = ((t - __ldg(a.qo + u)) * a.G + hq % a.G) / a.rows;
+  const int64_t at = (int64_t)before * a.Hkv + ((int64_t)tile * a.Hkv + hq / a.G) * steps;
+  return bal.block_of(at + steps - 1) - bal.block_of(at) + 1;
 }
 
 // Selected mode: items run over the queries, their row tiles, the chunks of
@@ -270,9 +358,9 @@ __device__ __forceinline__ bool find_selected(const AttendArgs& a, int rows, int
   it.slot = a.slot0 + c;
   it.k0 = c * a.chunk;
   it.k1 = min(a.k, it.k0 + a.chunk);
-  if (it.qb >= __ldg(a.qo + a.S)) return false;
+  const int live = __ldg(a.qo + a.S);
   it.seq = warp_segment(a.qo, a.S, it.qb);
-  return true;
+  return it.qb < live;
 }
 
 // Position of query t, or -1 (flagged) where it is outside its sequence.

@@ -32,6 +32,11 @@ WHOLE = [  # lens, queries, hq, hkv, dim, page, dtype, layout
     ([260, 100], _last([260, 100], 20), 10, 2, 128, 16, BF, {}),
     ([300, 500], [list(range(300)), list(range(100, 400))], 2, 1, 128, 48, BF, dict(heads_first=True)),
     ([400], [list(range(400))], 4, 2, 64, 16, FP, {}),
+    # long keys for few rows: cut into equal parts over all blocks
+    ([20000], [[19999]], 4, 1, 128, 64, BF, {}),
+    ([9000, 0, 3, 15001, 128], [[8998, 8999], [], [2], [15000, 7], [127]], 6, 2, 64, 33, FP, dict(pad_rows=1)),
+    ([7000] * 3 + [1, 5000], _last([7000] * 3 + [1, 5000], 2), 24, 1, 128, 16, BF, dict(packed=True)),
+    ([12000], [[3, 700, 11999]], 36, 1, 64, 16, BF, dict(heads_first=True)),
 ]
 
 
@@ -54,6 +59,8 @@ SHARED = [  # lens, queries per sequence, groups {first: (end, length)}, hq, hkv
     ([1300] * 9, 3, {0: (9, 1290)}, 32, 2, 64, 33, BF),
     ([50, 60], 1, {0: (2, 50)}, 2, 1, 128, 16, BF),                      # nothing of its own in the first
     ([50, 60, 70], 1, {0: (2, 0), 2: (3, 60)}, 2, 1, 128, 16, BF),       # an empty prefix, a group of one
+    ([9000, 9500, 900, 20000], 1, {0: (3, 640)}, 4, 1, 128, 64, BF),     # long ones of their own behind it
+    ([5000] * 6 + [400], 2, {0: (3, 4096), 3: (7, 300)}, 16, 2, 64, 16, FP),
 ]
 
 
