@@ -280,8 +280,9 @@ typedef struct {
 /* Sequences that begin with the same tokens: those of group g are
  * seq_offsets[g] .. seq_offsets[g+1]-1, and their first lens[g] tokens are
  * read once for all of them, at the place where the group's first sequence
- * keeps them (a length beyond that sequence's own, or beyond max_len, sets
- * MISA_STATUS_BAD_INPUT and is cut).  A sequence in no group shares nothing. */
+ * keeps them (a length below 0, beyond that sequence's own or beyond max_len
+ * sets MISA_STATUS_BAD_INPUT and is cut; with max_len 0 no length is read).
+ * A sequence in no group shares nothing. */
 typedef struct {
   int32_t num_groups;            /* >= 0 */
   int32_t max_len;               /* host-side upper bound on every length */

@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   const int wm = warp % WM, grp = warp / WM;
   const E tag = E();
 
+  if (MODE == kShared && blockIdx.x == 0) check_shared(a);
   const bool few = (MODE == kOwn ? a.S : a.ng) <= 32 && a.blocks == 0;
   int total = 0;
   if constexpr (MODE == kSelected) {
@@ -725,7 +726,7 @@ struct Plan {
   bool finish = false;  // the own launch writes the results, with what the shared one left
   bool partial = false;
   size_t o_bytes = 0, lse_bytes = 0;
-  size_t bytes() const { return partial ? o_bytes + lse_bytes : 256; }
+  size_t bytes() const { return partial ? o_bytes + lse_bytes + 256 : 256; }
 };
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -142,6 +142,12 @@ __device__ __forceinline__ int shared_len(const AttendArgs& a, int g) {
   return max(0, min(__ldg(a.slen + g), min(a.max_shared, seq_len(a, s0))));
 }
 
+// Flags lengths that shared_len cuts; by the threads of one block.
+__device__ __forceinline__ void check_shared(const AttendArgs& a) {
+  for (int g = threadIdx.x; g < a.ng; g += blockDim.x)
+    if (__ldg(a.slen + g) != shared_len(a, g)) set_status(a.status, MISA_STATUS_BAD_INPUT);
+}
+
 // The group of sequence s, or -1.
 __device__ __forceinline__ int group_of(const AttendArgs& a, int s) {
   if (a.ng == 0 || s < __ldg(a.so) || s >= __ldg(a.so + a.ng)) return -1;

@@ -254,6 +254,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
   volatile int* s_boxed = abort + 2;  // bit i: entry i of s_rows holds boxes
   int* s_sum = abort + 3;
   int total;
+  if (MODE == kShared && blockIdx.x == 0) check_shared(a);
   if constexpr (MODE == kSelected) {
     total = a.T * ((a.G + kRows - 1) / kRows) * a.nch_max;
   } else {

@@ -308,3 +308,139 @@ def test_a_step_as_it_is_used():
     assert torch.equal(torch.from_numpy(np.sort(idx, 1)), ix.idx.cpu().sort(1).values)
     b.check(out, lse, idx=ix.idx.cpu().numpy())
     assert (out.float() - want.float()).abs().max() <= 2.0 ** -6 * want.float().abs().max()
+
+
+@pytest.mark.parametrize("hq", [4, 56])                # warp-level and tcgen05 kernels
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 0.3])
+def test_scales_of_any_sign(hq, scale):
+    b = Batch([700, 333], _last([700, 333], 2), hq, 1, 128, 16, BF)
+    out, lse = b.attention(scale=scale)
+    assert_status_ok()
+    b.check(out, lse, scale=scale)
+    idx = _lists(b, 150, 1)
+    out, lse = b.selected(idx, scale=scale)
+    b.check(out, lse, idx=idx, scale=scale)
+
+
+@pytest.mark.parametrize("hq,n", [(4, 1), (8, 9)])
+def test_more_sequences_than_a_warp(hq, n):
+    g = np.random.default_rng(5)
+    lens = [int(x) for x in g.integers(n, 400, 70)]
+    b = Batch(lens, _last(lens, n), hq, 1, 64, 16, BF, seed=6, pad_rows=3)
+    out, lse = b.attention()
+    assert_status_ok()
+    b.check(out, lse)
+    # and as many groups: pairs of sequences that share, in turn with ones that do not
+    prefix = {s: (s + 2, min(lens[s], lens[s + 1]) // 2) for s in range(0, 69, 3)}
+    b = Batch(lens, _last(lens, n), hq, 1, 64, 16, BF, seed=6, pad_rows=3, prefix=prefix)
+    so, ln = [0], []
+    for s in range(0, 69, 3):
+        so += [s + 2, s + 3]
+        ln += [prefix[s][1], 0]
+    share = misa.SharedPrefix(so, ln)
+    out, lse = b.attention(share=share)
+    assert_status_ok()
+    b.check(out, lse)
+
+
+def test_shared_lengths_that_do_not_hold_are_flagged_and_cut():
+    for hq in (4, 64):
+        b = Batch([100, 120], _last([100, 120], 1), hq, 1, 64, 16, BF, prefix={0: (2, 100)})
+        share = misa.SharedPrefix([0, 2], [117], max_len=118)   # the first sequence has 100
+        out, lse = b.attention(share=share)
+        assert misa.stream_status()[1] == 0x4
+        b.check(out, lse)
+        share = misa.SharedPrefix([0, 2], [100], max_len=64)
+        out, lse = b.attention(share=share)
+        assert misa.stream_status()[1] == 0x4
+        b.check(out, lse)
+
+
+@pytest.mark.parametrize("hq", [4, 64])
+@pytest.mark.parametrize("extra", [8, 64, 136])
+def test_pages_with_gaps_between_them(hq, extra):
+    """Page strides that are no multiple of a row's elements, or only of their half."""
+    b = Batch([333, 90], _last([333, 90], 3), hq, 1, 128, 16, BF)
+    count = b.k.shape[0]
+    step = 16 * 128 + extra
+    k, v = (torch.full((count * step,), float("nan"), dtype=BF, device="cuda").as_strided((count, 16, 1, 128), (step, 128, 128, 1))
+            for _ in range(2))
+    k.copy_(b.k)
+    v.copy_(b.v)
+    b.cache = misa.KVCache(k, v, b.table_dev)
+    out, lse = b.attention()
+    assert_status_ok()
+    b.check(out, lse)
+    idx = _lists(b, 60, 2)
+    out, lse = b.selected(idx)
+    b.check(out, lse, idx=idx)
+
+
+def test_no_queries_and_no_tokens():
+    b = Batch([50, 0], [[], []], 4, 2)
+    out, lse = b.attention()
+    idx = np.zeros((0, 5), np.int32)
+    b.selected(idx)
+    assert_status_ok() is None and out.numel() == 0
+
+
+def test_two_streams_at_once():
+    """Different calls in flight together, each with a workspace of its own."""
+    batches = [Batch([20000, 500], _last([20000, 500], 2), 8, 1, 128, 64, BF, seed=1),
+               Batch([900, 1200], _last([900, 1200], 60), 8, 1, 128, 16, FP, seed=2),
+               Batch([3000], _last([3000], 3), 64, 1, 64, 16, BF, seed=3)]
+    idx = torch.from_numpy(_lists(batches[2], 700, 4)).cuda()
+    bufs = [b.buffers() for b in batches[:2]] + [batches[2].buffers(700)]
+
+    def run(i):
+        b, (out, lse, ws) = batches[i], bufs[i]
+        if i == 2:
+            misa.attention_selected(b.prob, b.cache, b.q, idx, out, ws, lse=lse)
+        else:
+            misa.attention(b.prob, b.cache, b.q, out, ws, lse=lse)
+
+    for i in range(3):
+        run(i)
+    torch.cuda.synchronize()
+    want = [(o.clone(), l.clone()) for o, l, _ in bufs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        for o, l, _ in bufs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                run(i)
+        torch.cuda.synchronize()
+        for (o, l, _), (wo, wl) in zip(bufs, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+    assert_status_ok()
+    batches[0].check(*bufs[0][:2])
+    batches[1].check(*bufs[1][:2])
+    batches[2].check(*bufs[2][:2], idx=idx.cpu().numpy())
+
+
+def test_one_workspace_in_two_graphs_of_one_stream():
+    b = Batch([9000, 4000], _last([9000, 4000], 2), 8, 1, 128, 64, BF)
+    c = Batch([700, 900], _last([700, 900], 70), 8, 1, 128, 64, BF, seed=9)
+    (o1, l1, w1), (o2, l2, w2) = b.buffers(), c.buffers()
+    ws = w1 if w1.numel() >= w2.numel() else w2
+    runs = [lambda: misa.attention(b.prob, b.cache, b.q, o1, ws, lse=l1),
+            lambda: misa.attention(c.prob, c.cache, c.q, o2, ws, lse=l2)]
+    graphs = []
+    for r in runs:
+        r()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r()
+        graphs.append(g)
+    for _ in range(3):
+        o1.zero_()
+        o2.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        b.check(o1, l1)
+        c.check(o2, l2)
+    assert_status_ok()
