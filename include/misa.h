@@ -316,7 +316,8 @@ int misa_cache_append(const misa_problem_t* p, const misa_kv_cache_t* cache, con
 
 /* Attention of every query over tokens 0..q_pos[t] of its sequence:
  *     out[t,h] = sum_s softmax_s(x[t,h,s]) v[s, h / (num_q_heads / num_kv_heads)]
- *   q, out [T, num_q_heads, head_dim] of the cache's type, contiguous;
+ *   q, out [T, num_q_heads, head_dim] of the cache's type, contiguous, no
+ *   overlap;
  *   num_q_heads a multiple of num_kv_heads, at most 64 times as many heads
  *   per key head; lse: NULL, or fp32 [T, num_q_heads] receiving
  *   ln sum_s exp(x).  A query that sees no token (a position outside its

@@ -338,8 +338,10 @@ class KVCache:
         if page_table is not None:
             t = page_table
             if (t.dtype != torch.int32 or t.dim() != 2 or t.device != k.device
-                    or (t.shape[1] > 1 and t.stride(1) != 1)):
-                _refuse(w, "page_table must be int32 [S, pages] on the cache's device, rows contiguous")
+                    or (t.shape[1] > 1 and t.stride(1) != 1)
+                    or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+                _refuse(w, "page_table must be int32 [S, pages] on the cache's device, rows contiguous "
+                           "and apart (an expanded table has no room of its own for each sequence)")
             self.seqs = t.shape[0]
             c.page_size, c.num_pages, c.page_stride = k.shape[1], k.shape[0], k.stride(0)
             c.pages_per_seq = t.shape[1]

@@ -444,3 +444,29 @@ def test_one_workspace_in_two_graphs_of_one_stream():
         b.check(o1, l1)
         c.check(o2, l2)
     assert_status_ok()
+
+
+@pytest.mark.parametrize("hq", [4, 64])
+def test_queries_inside_the_shared_prefix(hq):
+    lens, qs = [300, 280, 400], [[10, 299], [5, 130, 255], [256, 0]]
+    b = Batch(lens, qs, hq, 1, 128, 16, BF, prefix={0: (3, 256)})
+    share = misa.SharedPrefix([0, 3], [256])
+    opts = dict(softcap=20.0, slopes=_slopes(hq))
+    for kw in ({}, opts):
+        out, lse = b.attention(share=share, **kw)
+        assert_status_ok()
+        b.check(out, lse, **kw)
+
+
+def test_calls_that_python_or_the_library_refuse():
+    b = Batch([50, 40], _last([50, 40], 1), 4, 2)
+    with pytest.raises(ValueError, match="page_table"):
+        misa.KVCache(b.k, b.v, b.table_dev[:1].expand(2, -1))
+    out, lse, ws = b.buffers()
+    with pytest.raises(misa.MisaError, match="out must not be q"):
+        misa.attention(b.prob, b.cache, b.q, b.q, ws)
+    with pytest.raises(misa.MisaError, match="workspace too small"):
+        big = Batch([30000], [[29999]], 4, 1)
+        misa.attention(big.prob, big.cache, big.q, big.buffers()[0], ws)
+    b.attention()
+    assert_status_ok()
