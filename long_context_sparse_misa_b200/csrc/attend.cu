@@ -892,7 +892,6 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   if (p->num_queries == 0) return MISA_OK;
   if ((rc = check_ptr(q, 16, "q")) || (rc = check_ptr(out, 16, "out")) || (rc = check_ptr(ws, 256, "workspace")))
     return rc;
-  if (q == out) { set_error("out must not be q: blocks read q after others have written"); return MISA_ERR_INVALID_ARG; }
   if ((lse && !aligned(lse, 4)) || (opts->slopes && !aligned(opts->slopes, 4))) {
     set_error("lse or slopes misaligned");
     return MISA_ERR_INVALID_ARG;
@@ -902,6 +901,7 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
     set_error("workspace too small: %zu < %zu", ws_bytes, pl.bytes());
     return MISA_ERR_WORKSPACE_TOO_SMALL;
   }
+  if (q == out) { set_error("out must not be q: blocks read q after others have written"); return MISA_ERR_INVALID_ARG; }
   uint32_t* status = status_ptr();
   if (!status) { set_error("status word unavailable"); return MISA_ERR_CUDA; }
   AttendArgs a = {};
