@@ -23,10 +23,9 @@
 // swizzled: a tile of whole pages by TMA boxes, any other, and a selection, by
 // TMA gathers of four rows (a row that does not exist is out of the map's bounds
 // and comes as zeros).  A thread issues a gather in about 35 cycles, so two share
-// a tile; the copies themselves go on at more than twice what four issue (12.6
-// TB/s from L2 by four threads an SM, 17.9 by six).  Warp 14 looks over value
-// tiles that only some rows see (cut_infinite).  Blocks are persistent, and the
-// fetching warps run ahead into the next item.
+// a tile (gathers by one thread an SM read 3.2 TB/s from L2, by four 12.6).
+// Warp 14 looks over value tiles that only some rows see (cut_infinite).  Where a
+// block takes several items, the fetching warps run ahead into the next one.
 //
 // Bound by the chain of one tile (its S, two passes of softmax, P, the product:
 // about 4000 cycles, of which the other stream hides half): 2 x 1000 queries of
