@@ -345,7 +345,8 @@ class KVCache:
             self.seqs = t.shape[0]
             c.page_size, c.num_pages, c.page_stride = k.shape[1], k.shape[0], k.stride(0)
             c.pages_per_seq = t.shape[1]
-            c.page_table = t.data_ptr()
+            # an empty table's address is NULL, which would mean packed; with no entries it is not read
+            c.page_table = t.data_ptr() or c.k
             c.page_table_stride = max(t.stride(0), t.shape[1])
         self.ref = ctypes.byref(c)
 

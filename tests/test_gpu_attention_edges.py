@@ -1,0 +1,44 @@
+"""The cache and attention entry points on a B200 in corners of what their
+documentation allows: empty tables, padding rows that are not there, values
+that are not finite, caps and weights at the ends of their range."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_sparse_misa_b200 as misa
+from tests.attention_cases import Batch, assert_status_ok
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+BOUNDS, BAD_INPUT = 0x2, 0x4
+
+
+def _last(lens, n):
+    return [list(range(max(0, L - n), L)) for L in lens]
+
+
+def _slopes(hq):
+    return torch.tensor([2.0 ** (-8.0 * (i + 1) / hq) for i in range(hq)], device="cuda")
+
+
+def _bits(x):
+    return x.contiguous().view(torch.int16)
+
+
+@pytest.mark.parametrize("hq", [4, 64])                # warp-level and tcgen05 kernels
+def test_a_page_table_without_entries_has_room_for_no_token(hq):
+    b = Batch([40, 23], _last([40, 23], 2), hq, 1, page=16)
+    cache = misa.KVCache(b.k, b.v, b.table_dev[:, :0])
+    before = b.k.clone(), b.v.clone()
+    new = torch.ones(b.T, 1, 128, dtype=BF, device="cuda")
+    misa.cache_append(b.prob, cache, new, new)
+    assert misa.stream_status()[1] == BOUNDS
+    assert torch.equal(_bits(b.k), _bits(before[0])) and torch.equal(_bits(b.v), _bits(before[1]))
+    b.cache = cache
+    out, lse = b.attention()
+    assert misa.stream_status()[1] == BOUNDS
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    out, lse = b.selected(np.tile(np.arange(5, dtype=np.int32), (b.T, 1)))
+    assert misa.stream_status()[1] == BOUNDS
+    assert (out == 0).all() and (lse == -float("inf")).all()
