@@ -4,15 +4,16 @@
 // k[t] turned by p's angles; q_out[t] receives q[t] turned by the same.  Each
 // pair (x, y) becomes (x cos - y sin, y cos + x sin), in fp32, rounded once.
 // Bandwidth-bound: every element is read once and written once (32768 tokens
-// of 32 + 2 * 8 heads: 163 us, 5.0 TB/s; 227 us with the loads behind the lookup).
+// of 32 + 2 * 8 heads: 167 us, 4.9 TB/s; 227 us with the loads behind the lookup).
 //
 // An item is 16 elements of one head (eight pairs): two 16-byte loads, two
 // 16-byte stores and the pairs' eight cosines and sines, which the heads of a
 // token share through L1.  A thread block takes `tokens` consecutive tokens,
 // about one round of kUnroll items a thread.  What an item reads depends on its
-// number alone, so its loads go out first, and the block's warps find each
-// token's sequence, position and cache row (a chain of up to four loads) while
-// they are under way.
+// number alone, so its loads go out as soon as the block knows how many of its
+// tokens are not padding (one load, 0.1 us of a step of 16 x 3 tokens' 4.1), and
+// the block's warps find each token's sequence, position and cache row (a chain
+// of up to four loads) while they are under way.
 #include "cache.cuh"
 
 namespace misa {
@@ -142,7 +143,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
   __shared__ int64_t s_row[kAppendTokens];
   __shared__ int s_pos[kAppendTokens];
   const int t0 = blockIdx.x * a.tokens;
-  const int nt = min(a.tokens, a.T - t0);
+  // rows behind the last sequence's are padding, which need not be there: none is read
+  const int nt = min(a.tokens, min(a.T, __ldg(a.qo + a.S)) - t0);
+  if (nt <= 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kPer = D / 16;  // items of a head
   const int heads = a.Hq + a.Hkv + (a.v ? a.Hkv : 0);
@@ -180,33 +183,26 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
   };
   load(threadIdx.x);
 
-  const int live = __ldg(a.qo + a.S);
   for (int i = warp; i < nt; i += kAppendThreads / 32) {
     const int t = t0 + i;
-    int pos = -1;
-    int64_t row = -1;
-    if (t < live) {
-      const int at = __ldg(a.q_pos + t);
-      const int seq = warp_segment(a.qo, a.S, t);
-      if (lane == 0) {
-        pos = at;
-        const int64_t len = __ldg(a.c.ko + seq + 1) - __ldg(a.c.ko + seq);
-        uint32_t bad = 0;
-        if (pos < 0 || pos >= len) {
-          bad = MISA_STATUS_BAD_INPUT;
-        } else if (a.rope && pos >= a.rope_rows) {
-          bad = MISA_STATUS_BOUNDS;
-        } else {
-          row = cache_row(a.c, seq, pos);
-          if (row < 0) bad = MISA_STATUS_BOUNDS;
-        }
-        if (bad) {
-          set_status(a.status, bad);
-          pos = -1;
-        }
-      }
-    }
+    int pos = __ldg(a.q_pos + t);
+    const int seq = warp_segment(a.qo, a.S, t);
     if (lane == 0) {
+      const int64_t len = __ldg(a.c.ko + seq + 1) - __ldg(a.c.ko + seq);
+      int64_t row = -1;
+      uint32_t bad = 0;
+      if (pos < 0 || pos >= len) {
+        bad = MISA_STATUS_BAD_INPUT;
+      } else if (a.rope && pos >= a.rope_rows) {
+        bad = MISA_STATUS_BOUNDS;
+      } else {
+        row = cache_row(a.c, seq, pos);
+        if (row < 0) bad = MISA_STATUS_BOUNDS;
+      }
+      if (bad) {
+        set_status(a.status, bad);
+        pos = -1;
+      }
       s_pos[i] = pos;
       s_row[i] = row;
     }

@@ -42,3 +42,20 @@ def test_a_page_table_without_entries_has_room_for_no_token(hq):
     out, lse = b.selected(np.tile(np.arange(5, dtype=np.int32), (b.T, 1)))
     assert misa.stream_status()[1] == BOUNDS
     assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("live,pad", [(1, 2500), (700, 1300), (1200, 1), (0, 900)])
+def test_append_with_blocks_of_padding_rows(live, pad):
+    """Blocks that hold some padding rows, or nothing else; what those rows hold goes nowhere."""
+    b = Batch([live + 5, 9], [list(range(live)), []], 2, 1, dim=64, page=16, pad_rows=pad)
+    x = torch.randn(b.rows, 4, 64, device="cuda").to(BF)
+    x[live:] = float("nan")
+    q_out = torch.full((b.rows, 2, 64), 9.0, dtype=BF, device="cuda")
+    want_k, want_v = b.k.clone(), b.v.clone()
+    at = torch.arange(live, device="cuda")
+    page = b.table_dev[0, at // 16].long()
+    want_k[page, at % 16], want_v[page, at % 16] = x[:live, 2:3], x[:live, 3:4]
+    misa.cache_append(b.prob, b.cache, x[:, 2:3], x[:, 3:4], q=x[:, :2], q_out=q_out)
+    assert_status_ok()
+    assert torch.equal(_bits(b.k), _bits(want_k)) and torch.equal(_bits(b.v), _bits(want_v))
+    assert torch.equal(q_out[:live], x[:live, :2]) and (q_out[live:] == 9).all()
