@@ -509,13 +509,15 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         fa = 0.f;  // no keys: nothing to exchange, and the other stream may still read the last item's
         lse2 = -INFINITY;
       } else {
-        s_ml[x * kTile + r] = make_float2(ref, l);
+        // a stream without tiles leaves nothing: it has not waited for a product of this item, so the
+        // other may still be reading what the last item's rows left in its place
+        if (mine > 0) s_ml[x * kTile + r] = make_float2(ref, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full);
         if (!warp_wait(ml_full, n_ml & 1, abort, a.status)) break;
         ++n_ml;
-        const float2 ma = s_ml[r], mb = s_ml[kTile + r];
+        const float2 ma = s_ml[r], mb = s.n > 1 ? s_ml[kTile + r] : make_float2(-INFINITY, 0.f);
         const float m = fmaxf(ma.x, mb.x), base = m == -INFINITY ? 0.f : m;
         fa = ma.y == 0.f ? 0.f : ex2(ma.x - base);
         fb = mb.y == 0.f ? 0.f : ex2(mb.x - base);

@@ -59,3 +59,26 @@ def test_append_with_blocks_of_padding_rows(live, pad):
     assert_status_ok()
     assert torch.equal(_bits(b.k), _bits(want_k)) and torch.equal(_bits(b.v), _bits(want_v))
     assert torch.equal(q_out[:live], x[:live, :2]) and (q_out[live:] == 9).all()
+
+
+@pytest.mark.parametrize("k", [100, 200, 300])          # one, two and three tiles: even and odd shares of the two streams
+@pytest.mark.parametrize("dim", [64, 128])
+def test_blocks_that_take_many_lists_in_turn(k, dim):
+    """More tcgen05 items than blocks, with queries that see nothing between them."""
+    b = Batch([350, 200], [[300 + t % 50 for t in range(700)], [199] * 5], 48, 1, dim, 16, BF)
+    g = np.random.default_rng(k)
+    idx = np.stack([g.permutation(301)[:k] if t < 700 else g.permutation(400)[:k] % 200 for t in range(b.T)]).astype(np.int32)
+    blind = np.arange(3, 700, 7)
+    idx[blind[::2]] = -1
+    b.prob.q_pos[torch.from_numpy(blind[1::2].copy()).cuda()] = -1
+    out, lse = b.selected(idx)
+    assert misa.stream_status()[1] == BAD_INPUT
+    assert (out[blind] == 0).all() and (lse[blind] == -float("inf")).all()
+    b.check(out, lse, idx=idx, rows=[t for t in range(0, b.T, 23) if t not in blind] + list(range(700, 705)))
+    for t in range(2, 9):                               # other rows: the same list alone gives the same bits
+        one = np.full_like(idx, -1)
+        one[t * 50] = idx[t * 50]
+        if t * 50 not in blind:
+            alone, l1 = b.selected(one)
+            assert torch.equal(alone[t * 50], out[t * 50]) and torch.equal(l1[t * 50], lse[t * 50])
+    misa.stream_status()
