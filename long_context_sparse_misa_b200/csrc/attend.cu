@@ -366,18 +366,27 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         if (cut) *s_cut = 1;
         group_sync<WM>(grp);
       }
+      if constexpr (KIND == kCapped) {
+        // four values of one row, of two neighbouring key blocks: what is not a number stays in its row
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          if (mask) {
+#pragma unroll
+            for (int j = n; j < n + 2; ++j) {
+              const int2 kp = *reinterpret_cast<const int2*>(keys + st * KB + j * 8 + (lane & 3) * 2);
+              if (kp.x < 0 || kp.x > pos0) s[j][0] = 0.f;
+              if (kp.y < 0 || kp.y > pos0) s[j][1] = 0.f;
+              if (kp.x < 0 || kp.x > pos1) s[j][2] = 0.f;
+              if (kp.y < 0 || kp.y > pos1) s[j][3] = 0.f;
+            }
+          }
+          cap4(s[n][0], s[n][1], s[n + 1][0], s[n + 1][1], a);
+          cap4(s[n][2], s[n][3], s[n + 1][2], s[n + 1][3], a);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        if constexpr (KIND == kCapped) {
-          if (mask) {
-            const int2 kp = *reinterpret_cast<const int2*>(keys + st * KB + n * 8 + (lane & 3) * 2);
-            if (kp.x < 0 || kp.x > pos0) s[n][0] = 0.f;
-            if (kp.y < 0 || kp.y > pos0) s[n][1] = 0.f;
-            if (kp.x < 0 || kp.x > pos1) s[n][2] = 0.f;
-            if (kp.y < 0 || kp.y > pos1) s[n][3] = 0.f;
-          }
-          cap4(s[n][0], s[n][1], s[n][2], s[n][3], a);
-        } else {
+        if constexpr (KIND != kCapped) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[n][j] *= a.scale2;
         }

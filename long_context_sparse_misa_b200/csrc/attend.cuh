@@ -106,7 +106,8 @@ __device__ __forceinline__ float min_nan(float x, float y) {
 // cap near zero, where tanh.approx would be off by 2^-11.  The four quotients
 // share one reciprocal (1 / x = y z w / (x y z w)); e^{2u} is held at 2^30 (tanh
 // is 1 to fp32 from 2^26 on), so that the product stays in range.  A NaN makes
-// all four NaN: places that a row does not see are set to 0 before.
+// all four NaN, so they are four of one row, whose result it makes NaN anyway;
+// places that the row does not see are set to 0 before.
 __device__ __forceinline__ void cap4(float& x0, float& x1, float& x2, float& x3, const AttendArgs& a) {
   const uint64_t sc = pair(a.scale2, a.scale2), one = pair(1.f, 1.f), c = pair(a.cap2, a.cap2);
   float y0, y1, y2, y3, m0, m1;

@@ -82,3 +82,83 @@ def test_blocks_that_take_many_lists_in_turn(k, dim):
             alone, l1 = b.selected(one)
             assert torch.equal(alone[t * 50], out[t * 50]) and torch.equal(l1[t * 50], lse[t * 50])
     misa.stream_status()
+
+
+# ---------------------------------------------------------------- what is not finite, under a cap
+ROWS = [(4, 1), (16, 1), (8, 3), (32, 2), (8, 20), (48, 1)]  # query heads on one key head, queries: 4 to 160 rows
+
+
+@pytest.mark.parametrize("hq,n", ROWS)
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_a_nan_in_one_row_of_q_stays_there_under_a_cap(hq, n, dt):
+    b = Batch([400, 333], _last([400, 333], n), hq, 1, page=16, dtype=dt)
+    opts = dict(softcap=20.0, slopes=_slopes(hq))
+    idx = np.stack([np.arange(150, dtype=np.int32)] * b.T)
+    for run in (lambda: b.attention(**opts), lambda: b.selected(idx, **opts)):
+        clean, lse = run()
+        assert_status_ok()
+        for t, h in ((0, 0), (b.T - 1, hq // 2), (n // 2, hq - 1)):
+            kept = b.q[t, h].clone()
+            b.q[t, h, 5] = float("nan")
+            out, lse2 = run()
+            b.q[t, h] = kept
+            assert out[t, h].isnan().all() and lse2[t, h].isnan()
+            out[t, h], lse2[t, h] = clean[t, h], lse[t, h]
+            assert torch.equal(out, clean) and torch.equal(lse2, lse), (t, h)
+    assert_status_ok()
+
+
+@pytest.mark.parametrize("seqs,hq", [(4, 4), (12, 2), (3, 16), (40, 4)])
+def test_a_nan_in_one_sequence_stays_there_under_a_cap_with_a_shared_prefix(seqs, hq):
+    lens = [260 + 7 * (s % 5) for s in range(seqs)]
+    b = Batch(lens, _last(lens, 1), hq, 1, page=16, prefix={0: (seqs, 256)})
+    share = misa.SharedPrefix([0, seqs], [256])
+    clean, lse = b.attention(share=share, softcap=30.0)
+    assert_status_ok()
+    for t in (0, seqs // 2, seqs - 1):
+        kept = b.q[t].clone()
+        b.q[t, 0, 100] = float("nan")
+        out, lse2 = b.attention(share=share, softcap=30.0)
+        b.q[t] = kept
+        assert out[t, 0].isnan().all() and lse2[t, 0].isnan()
+        out[t, 0], lse2[t, 0] = clean[t, 0], lse[t, 0]
+        assert torch.equal(out, clean) and torch.equal(lse2, lse), t
+
+
+@pytest.mark.parametrize("hq,n", ROWS)
+def test_an_infinite_key_is_a_capped_score(hq, n):
+    """Infinities give the cap or minus the cap, as any product far beyond it does; only a row whose
+    query has a zero there gets a NaN.  Rows of a tile that do not exist hold zeros."""
+    b = Batch([400, 333], _last([400, 333], n), hq, 1, page=16)
+    b.q[b.T - 1, hq - 1, 9] = 0
+    at = int(b.table[0, 2]), 5
+    idx = np.stack([np.arange(150, dtype=np.int32)] * b.T)
+    for run in (lambda: b.attention(softcap=15.0), lambda: b.selected(idx, softcap=15.0)):
+        for sign in (1.0, -1.0):
+            for s in range(2):
+                at = int(b.table[s, 2]), 5
+                b.k[at][0, 9] = sign * 2.0 ** 60
+            want, wl = run()
+            for s in range(2):
+                at = int(b.table[s, 2]), 5
+                b.k[at][0, 9] = sign * float("inf")
+            out, lse = run()
+            assert out[b.T - 1, hq - 1].isnan().all()
+            out[b.T - 1, hq - 1], lse[b.T - 1, hq - 1] = want[b.T - 1, hq - 1], wl[b.T - 1, hq - 1]
+            assert torch.equal(out, want) and torch.equal(lse, wl)
+    assert_status_ok()
+
+
+@pytest.mark.parametrize("hq,n", [(2, 3), (8, 2), (16, 3), (16, 2), (4, 150)])
+def test_what_the_last_token_holds_reaches_no_earlier_query_under_a_cap(hq, n):
+    b = Batch([400, 333], _last([400, 333], n), hq, 1, page=16)
+    clean, lse = b.attention(softcap=20.0)
+    for s, L in enumerate(b.lens):
+        at = int(b.table[s, (L - 1) // 16]), (L - 1) % 16
+        b.k[at], b.v[at] = float("nan"), float("inf")
+    out, lse2 = b.attention(softcap=20.0)
+    assert_status_ok()
+    early = [t for t in range(b.T) if b.pos[t] < b.lens[b.seq[t]] - 1]
+    assert torch.equal(out[early], clean[early]) and torch.equal(lse[early], lse2[early])
+    late = [t for t in range(b.T) if b.pos[t] == b.lens[b.seq[t]] - 1]
+    assert out[late].isnan().all()
