@@ -270,10 +270,12 @@ typedef struct {
 /* What happens to a product before the softmax:
  *     x = scale * (q . k[s]);   softcap > 0: x = softcap * tanh(x / softcap);
  *     slopes != NULL: x -= slopes[head] * (q_pos[t] - s).
- * An x of -inf counts as masked; a NaN reaches the row's output. */
+ * An x of -inf counts as masked; a NaN reaches the row's output, and no other
+ * row's.  A cap up to 64 puts x off by at most 2^-20 softcap, a larger one by at
+ * most 3 2^-20 |x|, however large: a cap far above the scores is as none. */
 typedef struct {
   float scale;
-  float softcap;                 /* 0: none */
+  float softcap;                 /* 0: none, else any finite value > 0 */
   const float* slopes;           /* device fp32 [num_q_heads], or NULL */
 } misa_attention_opts_t;
 

@@ -22,6 +22,7 @@
 #include "attend.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <numeric>
 
@@ -380,8 +381,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
               if (kp.y < 0 || kp.y > pos1) s[j][3] = 0.f;
             }
           }
-          cap4(s[n][0], s[n][1], s[n + 1][0], s[n + 1][1], a);
-          cap4(s[n][2], s[n][3], s[n + 1][2], s[n + 1][3], a);
+          if (a.wide) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cap_wide(s[n + (j >> 2)][j & 3], a);
+          } else {
+            cap4(s[n][0], s[n][1], s[n + 1][0], s[n + 1][1], a);
+            cap4(s[n][2], s[n][3], s[n + 1][2], s[n + 1][3], a);
+          }
         }
       }
 #pragma unroll
@@ -924,8 +930,13 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   a.slopes = opts->slopes;
   a.status = status;
   const bool cap = opts->softcap > 0.f;
-  a.scale2 = cap ? 2.f * opts->scale / opts->softcap * kLog2e : opts->scale * kLog2e;
-  a.cap2 = cap ? opts->softcap * kLog2e : 0.f;
+  // held finite, so that a product of 0 stays 0; a cap's rows then stay finite too
+  auto finite = [](double x, double most) { return (float)std::max(-most, std::min(most, x)); };
+  const double log2e = 1.4426950408889634, raw2 = opts->scale * log2e;
+  a.raw2 = finite(raw2, FLT_MAX);
+  a.scale2 = cap ? finite(2 * raw2 / opts->softcap, FLT_MAX) : a.raw2;
+  a.cap2 = cap ? finite(opts->softcap * log2e, FLT_MAX / 4) : 0.f;
+  a.wide = opts->softcap > kWideCap;
   const RowGrid grid = row_grid(p, c);
   if (grid.rows) {
     // a stride that nothing is multiplied by need not be a multiple of the unit

@@ -28,6 +28,8 @@ struct AttendArgs {
   uint32_t* status;
   float scale2;        // no cap: scale * log2(e); cap: 2 * scale / cap * log2(e)
   float cap2;          // cap * log2(e), or 0
+  float raw2;          // scale * log2(e), for a wide cap
+  int wide;            // the cap is past kWideCap
   int S, T, Hq, Hkv, G, k, ng, max_shared, max_seq_len;
   int chunk, nch_max;  // keys of an item; most items along the keys
   int64_t unit;        // the tensor core kernel's rows: elements between them (divides every stride),
@@ -62,7 +64,10 @@ __device__ __forceinline__ float rcp(float x) {
 
 // What is done to a product before the softmax, a kernel each: a cap's two
 // more special-function results per element would otherwise be paid by all.
-enum Change { kScaled = 0, kBiased = 1, kCapped = 2 /* and a bias, if there are slopes */ };
+// A cap past kWideCap is a kind of its own on tcgen05, where the mere presence of
+// its code costs ordinary caps 14 of 150 us (the prefix of 64 sequences behind
+// 32768 shared); the warp-level kernel branches, for 0.3 of 7 (64 lists of 256).
+enum Change { kScaled = 0, kBiased = 1, kCapped = 2 /* and a bias, if there are slopes */, kWideCapped = 3 };
 
 // Three-way maximum; NaN if any is.
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -102,8 +107,8 @@ __device__ __forceinline__ float min_nan(float x, float y) {
 }
 
 // Four products -> capped exponents of 2.  cap tanh(u) is formed as
-// cap - 2 cap / (e^{2u} + 1): exact at both ends, and off by a rounding of the
-// cap near zero, where tanh.approx would be off by 2^-11.  The four quotients
+// cap - 2 cap / (e^{2u} + 1): exact at both ends, and off by up to 2^-20 of the
+// cap between, where tanh.approx would be off by 2^-11.  The four quotients
 // share one reciprocal (1 / x = y z w / (x y z w)); e^{2u} is held at 2^30 (tanh
 // is 1 to fp32 from 2^26 on), so that the product stays in range.  A NaN makes
 // all four NaN, so they are four of one row, whose result it makes NaN anyway;
@@ -120,6 +125,24 @@ __device__ __forceinline__ void cap4(float& x0, float& x1, float& x2, float& x3,
   const uint64_t q = pair(r * m1, r * m0);  // -2 cap / (e0 e2), -2 cap / (e1 e3)
   unpair(fma2(q, e23, c), x0, x1);
   unpair(fma2(q, e01, c), x2, x3);
+}
+
+// The same for a cap past kWideCap, from which on 2^-20 of the cap (6e-5 of an
+// exponent at 64) would show: where |u| < 0.35 the product times tanh(u) / u by
+// its Taylor series to u^10 (off by 2^-24), else the quotient, so that the error
+// is a share of the score, whatever the cap: 2^-21, and 3 2^-20 from the
+// quotient.  Ordinary caps keep cap4: 239 us where this takes 313 (64 sequences
+// behind 32768 shared).
+constexpr float kWideCap = 64.f;
+__device__ __forceinline__ void cap_wide(float& x, const AttendArgs& a) {
+  const float y = x * a.scale2, u = y * (0.5f * kLn2), w = u * u;
+  float t = fmaf(w, -1382.f / 155925.f, 62.f / 2835.f);
+  t = fmaf(w, t, -17.f / 315.f);
+  t = fmaf(w, t, 2.f / 15.f);
+  t = fmaf(w, t, -1.f / 3.f);
+  t = fmaf(w, t, 1.f);
+  const float q = fmaf(-2.f * a.cap2, rcp(ex2(min_nan(y, 30.f)) + 1.f), a.cap2);
+  x = fabsf(u) < 0.35f ? x * a.raw2 * t : q;
 }
 
 // Row of the cache seen as [map_rows, D], head 0, or -1: place `off` of page `pg`, or, packed,

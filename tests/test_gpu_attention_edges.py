@@ -162,3 +162,55 @@ def test_what_the_last_token_holds_reaches_no_earlier_query_under_a_cap(hq, n):
     assert torch.equal(out[early], clean[early]) and torch.equal(lse[early], lse2[early])
     late = [t for t in range(b.T) if b.pos[t] == b.lens[b.seq[t]] - 1]
     assert out[late].isnan().all()
+
+
+# ---------------------------------------------------------------- caps of any size
+def _check_cap(b, out, lse, idx=None, rows=None, softcap=0.0, scale=None, slopes=None):
+    """Batch.check with a bound that does not grow with the cap.
+
+    Half steps as there.  An exponent is off by dim 2^-22 sum |q k| scale for its product (the cap
+    makes no error larger), 2^-20 (max |x| + 1) for the bias, the exponential and the joining, and for
+    the cap itself by a share of |x|: its series by 8 roundings (2^-21); its quotient 2 cap / (e + 1),
+    at most 2 cap, by 8 roundings and the exponential's 2^-22, so 2^-20 cap in all, where |x| is at least
+    cap tanh(0.35) = 0.336 cap: 3 2^-20 |x|.  Together under 2^-18 (max |x| + 1)."""
+    from oracle import attention as plain
+    from tests.attention_cases import HALF_STEP
+    u = HALF_STEP[b.dtype]
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    f = lambda x: x.float().numpy()
+    scale = b.dim ** -0.5 if scale is None else scale
+    s_host = None if slopes is None else slopes.double().cpu().numpy()
+    for t in range(b.T) if rows is None else rows:
+        s, pos = b.seq[t], b.pos[t]
+        tok = np.arange(pos + 1) if idx is None else idx[t][(idx[t] >= 0) & (idx[t] <= pos)]
+        want, wl, spread, reach, top = plain.attend(f(b.q_host[t]), f(b.tok_k[s])[tok], f(b.tok_v[s])[tok], pos, tok,
+                                                    scale, softcap, s_host)
+        d = b.dim * 2.0 ** -22 * reach + 2.0 ** -18 * (top + 1)
+        assert (d < 0.1).all()                           # the bound below is of first order
+        tol = (u + 2.2 * d[:, None]) * spread + u * np.abs(want) * (1 + u) + 1e-30
+        if b.dtype == FP:
+            tol = tol + 2.0 ** -25 * (1 + np.abs(f(b.tok_v[s])[tok]).sum(0).max())
+        err = np.abs(o[t] - want)
+        assert (err <= tol).all(), f"row {t}: {(err / tol).max():.2f} x its bound"
+        assert (np.abs(l[t] - wl) <= 2.2 * d + 2.0 ** -20 * np.abs(wl)).all(), f"row {t}: lse"
+
+
+CAPS = [(65.0, None), (65.0, 1.5), (200.0, 3.0), (200.0, -3.0), (1e3, None), (1e3, 3.0), (1e4, None), (1e6, None), (1e8, None),
+        (3e38, None), (1e-3, None), (1e-30, None), (1e-40, None)]
+
+
+@pytest.mark.parametrize("softcap,scale", CAPS)
+@pytest.mark.parametrize("hq,n,dt", [(4, 2, FP), (16, 1, BF), (48, 1, FP), (4, 40, BF)])
+def test_caps_of_any_size(softcap, scale, hq, n, dt):
+    b = Batch([300, 131], _last([300, 131], n), hq, 1, 64, 16, dt, seed=3)
+    b.q_host[0, 1] = 0                                   # products of 0 stay 0, whatever the cap
+    b.q = b.q_host.cuda()
+    rows = sorted({0, 1, b.T // 2, b.T - 1})
+    opts = dict(softcap=softcap, scale=scale, slopes=_slopes(hq))
+    out, lse = b.attention(**opts)
+    assert_status_ok()
+    _check_cap(b, out, lse, rows=rows, **opts)
+    idx = np.stack([np.arange(120, dtype=np.int32)] * b.T)
+    out, lse = b.selected(idx, softcap=softcap, scale=scale)
+    assert misa.stream_status()[1] == (BAD_INPUT if (b.pos < 119).any() else 0)  # some lists name tokens ahead
+    _check_cap(b, out, lse, idx=idx, rows=rows, softcap=softcap, scale=scale)
