@@ -423,9 +423,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
       t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
       // a row that has seen nothing yet keeps 0 as its reference: 2^(-inf - 0) = 0
-      const float r0 = t0 == -INFINITY ? 0.f : t0, r1 = t1 == -INFINITY ? 0.f : t1;
+      const float r0 = t0 == -INFINITY ? 0.f : reference<E, 0>(t0), r1 = t1 == -INFINITY ? 0.f : reference<E, 0>(t1);
       if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {
-        const float c0 = ex2(m0 - r0), c1 = ex2(m1 - r1);
+        const float c0 = ex2(reference<E, 0>(m0) - r0), c1 = ex2(reference<E, 0>(m1) - r1);
         l0 *= c0;
         l1 *= c1;
 #pragma unroll
@@ -483,9 +483,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       }
       if ((lane & 3) == 0) {
         float* ml = s_ml + (grp * Sh::rows) * 2;
-        ml[row0 * 2] = m0;
+        ml[row0 * 2] = reference<E, 0>(m0);
         ml[row0 * 2 + 1] = l0;
-        ml[row1 * 2] = m1;
+        ml[row1 * 2] = reference<E, 0>(m1);
         ml[row1 * 2 + 1] = l1;
       }
     }

@@ -145,6 +145,20 @@ __device__ __forceinline__ void cap_wide(float& x, const AttendArgs& a) {
   x = fabsf(u) < 0.35f ? x * a.raw2 * t : q;
 }
 
+// What a row's exponents are taken from, given its maximum (or, on tcgen05, what
+// stands for it).  fp16 holds full precision down to 2^-14 only, so its weights
+// are kept up to 2^15 instead of 1: kAbove more than that maximum lets them grow
+// to.  A weight of 2^-29 of the largest then still rounds by half a step (2^-21
+// on tcgen05, whose rows may outgrow their reference by 2^8), where without it
+// 100000 weights of 2^-23.4, 1% of the mass, were off by a third each.  Maxima
+// past 2^20 have no bits left for it.  The sum takes the same weights, so the
+// results do not depend on it.
+template <typename E, int kAbove>
+__device__ __forceinline__ float reference(float m) {
+  if constexpr (std::is_same<E, __half>::value) return fabsf(m) < 1048576.f ? m - (15 - kAbove) : m;
+  return m;
+}
+
 // Row of the cache seen as [map_rows, D], head 0, or -1: place `off` of page `pg`, or, packed,
 // token `pos` of the sequence whose first is `first`.
 __device__ __forceinline__ int cache_unit(const AttendArgs& a, int64_t first, int pos, int pg, int off) {

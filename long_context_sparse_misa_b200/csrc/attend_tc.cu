@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kTcThreads = 512;
 constexpr int kTile = 128;          // keys of a tile, rows of a stream
-constexpr float kSlack = 8.f;       // log2 of how far a row's maximum may outgrow its reference
+constexpr int kAbove = 8;           // log2 of how far a row's maximum may outgrow its reference
 constexpr int kPrep = 2;            // tiles whose rows have been found and not been fetched
 constexpr int kKeep = 8;            // tiles whose key masks are kept
 
@@ -442,9 +442,9 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         top *= sc;  // sc > 0: -inf stays
         // an infinite or undefined exponent makes the row's results undefined
         if (!(top < INFINITY)) top = __int_as_float(0x7fffffff);
-        const bool grow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY) || top != top;
+        const bool grow = top > ref + kAbove || (ref == -INFINITY && top > -INFINITY) || top != top;
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(ref - top) : 1.f;  // 0 while nothing had been seen
+          const float f = grow ? ex2(reference<E, kAbove>(ref) - reference<E, kAbove>(top)) : 1.f;  // 0 while nothing had been seen
           if (grow) ref = top;
           l01 = mul2(l01, pair(f, f));
           if (i > 0) {
@@ -460,7 +460,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
             }
           }
         }
-        const float minus = ref == -INFINITY ? 0.f : -ref;
+        const float minus = ref == -INFINITY ? 0.f : -reference<E, kAbove>(ref);
         const uint64_t minus2 = pair(minus, minus);
         auto weigh = [&](int q, const float (&u)[32]) {
           uint32_t p[16];
@@ -497,6 +497,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         }
       }
       if (!ok) break;
+      ref = reference<E, kAbove>(ref);
       float l0, l1;
       unpair(l01, l0, l1);
       float l = l0 + l1;

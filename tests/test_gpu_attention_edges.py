@@ -214,3 +214,49 @@ def test_caps_of_any_size(softcap, scale, hq, n, dt):
     out, lse = b.selected(idx, softcap=softcap, scale=scale)
     assert misa.stream_status()[1] == (BAD_INPUT if (b.pos < 119).any() else 0)  # some lists name tokens ahead
     _check_cap(b, out, lse, idx=idx, rows=rows, softcap=softcap, scale=scale)
+
+
+# ---------------------------------------------------------------- many small weights behind a large one
+@pytest.mark.parametrize("nats", [16.23, 17.0, 18.5])
+@pytest.mark.parametrize("heads,grp,seqs,sink", [(8, 1, 64, 0), (4, 48, 40, -1), (4, 48, 40, 0)])
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_many_small_weights_behind_a_large_one(nats, heads, grp, seqs, sink, listed, dt):
+    """One token with a value of zero takes nearly all the weight, the others' small ones make the result.
+
+    N equal weights w = e^-x of the others, values c[d]: out = c N w / (1 + N w).  Each weight is rounded to
+    the type by half a step u of itself, or by half of fp16's smallest step, 2^-25: 2^-40 of the largest weight in
+    the warp-level kernel (weights up to 2^15), 2^-32 in the tcgen05 one (its reference times 2^7).  Its exponent
+    is off by d = 2^-22 dim x + 2^-20 (x + 1), fp32 sums of N / 16 terms at most by 2^-24 N / 16, the result by
+    half a step of its own."""
+    n = 65536 if listed else 100000
+    dim, page, hq = 64, 64, heads * grp
+    u = {BF: 2.0 ** -8, FP: 2.0 ** -11}[dt]
+    pages = -(-n // page)
+    k = torch.zeros(pages, page, heads, dim, dtype=dt, device="cuda")
+    c = (0.5 + torch.arange(dim) / 64).to(dt)
+    v = c.cuda().expand(pages, page, heads, dim).contiguous()
+    place = sink % n
+    k[place // page, place % page, :, 0] = nats
+    v[place // page, place % page] = 0
+    q = torch.zeros(seqs, hq, dim, dtype=dt, device="cuda")
+    q[:, :, 0] = 8.0
+    x = 8.0 * float(k[place // page, place % page, 0, 0]) / 8.0   # scale 1/8
+    prob = misa.Problem([n] * seqs, range(seqs + 1), [n - 1] * seqs, num_heads=1, block=64)
+    cache = misa.KVCache(k, v, torch.arange(pages, dtype=torch.int32, device="cuda").repeat(seqs, 1))
+    out, lse = torch.empty_like(q), torch.empty(seqs, hq, device="cuda")
+    ws = torch.empty(misa.attention_workspace_size(prob, cache, hq, n if listed else 0), dtype=torch.uint8, device="cuda")
+    if listed:
+        idx = torch.arange(n, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+        misa.attention_selected(prob, cache, q, idx, out, ws, lse=lse)
+    else:
+        misa.attention(prob, cache, q, out, ws, lse=lse)
+    assert_status_ok()
+    many = (n - 1) * np.exp(-x)
+    want = c.double().numpy() * many / (1 + many)
+    d = 2.0 ** -22 * dim * x + 2.0 ** -20 * (x + 1)
+    small = 0.0 if dt == BF else 2.0 ** -32 if grp >= 48 else 2.0 ** -40
+    tol = (u + 2.1 * d + 2.0 ** -24 * n / 16 + small * np.exp(x)) * want + u * want * (1 + u) + 2.0 ** -25
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol).all(), f"{(err / tol).max():.2f} x its bound, off by {(err / want).max():.4f} of the value"
+    assert (lse.double() - (x + np.log1p(many))).abs().max() <= 2.1 * d + 2.0 ** -20 * (x + 1)
