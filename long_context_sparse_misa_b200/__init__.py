@@ -614,14 +614,17 @@ class Indexer:
                slopes=None, stream=None):
         """Attention of q [T, heads, dim] over the tokens of the last selection
         (idx) in the key/value cache; returns out (a buffer of this object,
-        written anew by the next call, unless one is given)."""
+        written anew by the next call, unless one is given).  As the rest of this
+        object its calls share buffers: on several streams they must be ordered."""
         import torch
         size = attention_workspace_size(self.prob, cache, q.shape[1], self.k)
         # kept per shape for this object's life: a captured step finds its addresses again
         key = (tuple(q.shape), q.dtype, size)
         if key not in self._attend:
-            self._attend[key] = (torch.empty(size, dtype=torch.uint8, device=q.device),
-                                 torch.empty(q.shape, dtype=q.dtype, device=q.device))
+            # memory of the stream that will write it: what the current one freed may still be in use there
+            with torch.cuda.stream(stream):
+                self._attend[key] = (torch.empty(size, dtype=torch.uint8, device=q.device),
+                                     torch.empty(q.shape, dtype=q.dtype, device=q.device))
         ws, own = self._attend[key]
         out = own if out is None else out
         attention_selected(self.prob, cache, q, self.idx, out, ws, lse, scale, softcap,

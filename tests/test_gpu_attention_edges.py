@@ -260,3 +260,26 @@ def test_many_small_weights_behind_a_large_one(nats, heads, grp, seqs, sink, lis
     err = np.abs(out.double().cpu().numpy() - want)
     assert (err <= tol).all(), f"{(err / tol).max():.2f} x its bound, off by {(err / want).max():.4f} of the value"
     assert (lse.double() - (x + np.log1p(many))).abs().max() <= 2.1 * d + 2.0 ** -20 * (x + 1)
+
+
+# ---------------------------------------------------------------- groups and streams
+def test_attend_on_a_stream_of_its_own_takes_no_memory_that_is_still_written():
+    """The buffers that Indexer.attend makes at its first call belong to the stream it runs on: memory that
+    the current stream has freed, but not yet written for the last time, is not among them."""
+    b = Batch([900, 400], _last([900, 400], 2), 16, 2, 128, 16, BF)
+    prob = misa.Problem(b.lens, [0, 2, 4], b.pos, num_heads=8, block=64)
+    ix = misa.Indexer(prob, m=8, k=128)
+    ix.idx.copy_(torch.from_numpy(np.stack([np.arange(128, dtype=np.int32)] * 4)))
+    want, _ = b.selected(ix.idx.cpu().numpy())
+    q = b.q.repeat(1, 1, 1)
+    size = misa.attention_workspace_size(prob, b.cache, 16, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)                       # about 0.2 s
+    stale = [torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty_like(q)]
+    for x in stale:
+        x.fill_(0x7f)
+    del stale, x
+    out = ix.attend(q, b.cache, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
