@@ -284,7 +284,8 @@ typedef struct {
  * read once for all of them, at the place where the group's first sequence
  * keeps them (a length below 0, beyond that sequence's own or beyond max_len
  * sets MISA_STATUS_BAD_INPUT and is cut; with max_len 0 no length is read).
- * A sequence in no group shares nothing. */
+ * A sequence in no group shares nothing; the length of a group without
+ * sequences is not looked at. */
 typedef struct {
   int32_t num_groups;            /* >= 0 */
   int32_t max_len;               /* host-side upper bound on every length */

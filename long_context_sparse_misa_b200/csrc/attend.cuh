@@ -180,10 +180,12 @@ __device__ __forceinline__ int shared_len(const AttendArgs& a, int g) {
   return max(0, min(__ldg(a.slen + g), min(a.max_shared, seq_len(a, s0))));
 }
 
-// Flags lengths that shared_len cuts; by the threads of one block.
+// Flags lengths that shared_len cuts; by the threads of one block.  A group
+// without sequences has no first one to measure its length by, and nobody reads it.
 __device__ __forceinline__ void check_shared(const AttendArgs& a) {
   for (int g = threadIdx.x; g < a.ng; g += blockDim.x)
-    if (__ldg(a.slen + g) != shared_len(a, g)) set_status(a.status, MISA_STATUS_BAD_INPUT);
+    if (__ldg(a.so + g) < __ldg(a.so + g + 1) && __ldg(a.slen + g) != shared_len(a, g))
+      set_status(a.status, MISA_STATUS_BAD_INPUT);
 }
 
 // The group of sequence s, or -1.

@@ -263,6 +263,14 @@ def test_many_small_weights_behind_a_large_one(nats, heads, grp, seqs, sink, lis
 
 
 # ---------------------------------------------------------------- groups and streams
+def test_a_group_without_sequences_has_no_length_to_check():
+    b = Batch([100, 120], _last([100, 120], 1), 4, 1, 64, 16, BF, prefix={0: (2, 96)})
+    for so, ln in (([0, 2, 2], [96, 50]), ([0, 0, 2], [110, 96]), ([0, 0, 2, 2, 2], [120, 96, 5, 7])):
+        out, lse = b.attention(share=misa.SharedPrefix(so, ln))
+        assert_status_ok()
+        b.check(out, lse)
+
+
 def test_attend_on_a_stream_of_its_own_takes_no_memory_that_is_still_written():
     """The buffers that Indexer.attend makes at its first call belong to the stream it runs on: memory that
     the current stream has freed, but not yet written for the last time, is not among them."""
