@@ -82,8 +82,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// All 32 lanes wait together (abort == nullptr: to the limit, whatever else
-// has given up); the outcome is warp-uniform (so .sync.aligned
+// All 32 lanes wait together; the outcome is warp-uniform (so .sync.aligned
 // tcgen05 instructions that follow are executed by the whole warp or by none).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort,
                                           uint32_t* status, long long limit = kWaitCycles) {
@@ -95,10 +94,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* a
     if (__all_sync(0xffffffffu, done)) return true;
     int give_up = 0;
     if (lane == 0) {
-      if (abort && *reinterpret_cast<volatile int*>(abort)) {
+      if (*reinterpret_cast<volatile int*>(abort)) {
         give_up = 1;
       } else if (clock64() - t0 > limit) {
-        if (abort) *reinterpret_cast<volatile int*>(abort) = 1;
+        *reinterpret_cast<volatile int*>(abort) = 1;
         set_status(status, MISA_STATUS_TIMEOUT);
         give_up = 1;
       }
