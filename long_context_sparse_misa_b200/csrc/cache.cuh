@@ -64,10 +64,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
   return r;
 }
 
+// launch_pdl with clusters of `cluster` blocks along x (the grid is a multiple of it).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
+                               cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Argument checks (cache.cu).
 int check_batch(const misa_problem_t* p);
 int check_cache(const misa_problem_t* p, const misa_kv_cache_t* c, bool need_v);
 CacheView cache_view(const misa_problem_t* p, const misa_kv_cache_t* c);
+// Tensor map (abi.cu) of `rows` rows of `dim` 16-bit elements, `stride` elements apart, for gathers of
+// four rows of 64 elements.
+int make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim, int64_t stride, bool fp16);
 // Tensor map (abi.cu) of the cache as [pages, heads, page, dim], boxes of `box` rows of 64 elements.
 int make_box_map(CUtensorMap* map, const void* base, const CacheView& c, int heads, int dim, int box, bool fp16);
 

@@ -28,10 +28,6 @@ uint32_t* status_ptr();
 // tensor [rows, 128] with a {64, box_rows} box and 128-byte swizzle.
 int make_kmajor_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows);
 
-// The same for attention: `rows` rows of `dim` 16-bit elements, `stride`
-// elements apart, for gathers of four rows of 64 elements.
-int make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim, int64_t stride, bool fp16);
-
 int set_smem_limit(const void* kernel, int bytes);
 
 // Launches `kern` with programmatic dependent launch: its CTAs may be
@@ -51,26 +47,6 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-// The same with clusters of `cluster` blocks along x (the grid is a multiple of it).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
-                               cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 // SMs of the current device.
