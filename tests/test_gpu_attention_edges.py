@@ -291,3 +291,62 @@ def test_attend_on_a_stream_of_its_own_takes_no_memory_that_is_still_written():
     out = ix.attend(q, b.cache, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_no_queries_give_no_rows():
+    b = Batch([50, 0], [[], []], 4, 2)
+    out, lse = b.attention(softcap=3.0)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    out, lse = b.selected(np.zeros((0, 5), np.int32))
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    assert_status_ok()
+
+
+@pytest.mark.parametrize("hq", [4, 64])                # warp-level and tcgen05 kernels
+@pytest.mark.parametrize("dt,softcap", [(FP, 0.0), (BF, 90.0)])
+def test_sequences_that_end_inside_their_groups_prefix(hq, dt, softcap):
+    """They share what they have of it."""
+    lens, qs = [300, 100, 257, 17], [[299], [99, 3], [256, 255], [16]]
+    b = Batch(lens, qs, hq, 1, 64, 16, dt, pad_rows=2)
+    for s in range(1, 4):                               # read where the first sequence keeps them
+        n = min(lens[s], 256)
+        b.tok_k[s][:n], b.tok_v[s][:n] = b.tok_k[0][:n], b.tok_v[0][:n]
+    out, lse = b.attention(share=misa.SharedPrefix([0, 4], [256]), softcap=softcap)
+    assert_status_ok()
+    b.check(out, lse, softcap=softcap)
+
+
+@pytest.mark.parametrize("hq", [4, 64])
+@pytest.mark.parametrize("softcap", [0.0, 25.0, 5000.0])
+def test_a_padded_batch_in_a_graph_with_other_values(hq, softcap):
+    """Captured once, replayed on other queries; padding rows hold NaN and are left alone."""
+    b = Batch([700, 90], _last([700, 90], 2), hq, 1, 128, 16, FP, pad_rows=5)
+    b.q[b.T:] = float("nan")
+    out, lse, ws = b.buffers()
+    run = lambda o, l: misa.attention(b.prob, b.cache, b.q, o, ws, lse=l, softcap=softcap)
+    run(out, lse)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run(out, lse)
+    for seed in range(3):
+        b.q[:b.T] = torch.randn(b.T, hq, 128, generator=torch.Generator().manual_seed(seed)).to(FP).cuda()
+        want, wl, _ = b.buffers()
+        run(want, wl)
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert (out[b.T:] == 7).all() and (lse[b.T:] == 7).all() and out[:b.T].isfinite().all()
+    assert_status_ok()
+
+
+def test_wide_caps_come_close_to_none():
+    b = Batch([500, 200], _last([500, 200], 3), 16, 1, 128, 16, FP)
+    none, lse = b.attention()
+    wide, lse2 = b.attention(softcap=1e30)
+    assert_status_ok()
+    # the same exponents but for a rounding of each of their factors, some 2^-22 of at most 8
+    assert (lse - lse2).abs().max() <= 2.0 ** -17
+    assert (none.float() - wide.float()).abs().max() <= 2.0 ** -10 * none.float().abs().max()
