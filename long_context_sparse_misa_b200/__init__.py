@@ -325,8 +325,8 @@ class KVCache:
         dims = 3 if page_table is None else 4
         if k.dim() != dims or k.stride(-1) != 1:
             _refuse(w, f"k must have {dims} dimensions, the last contiguous, got {tuple(k.shape)}")
-        if v is not None and (v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype
-                              or v.device != k.device):
+        if v is not None and (v.shape != k.shape or v.dtype != k.dtype or v.device != k.device
+                              or any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride()))):
             _refuse(w, "v must have k's shape, strides, dtype and device")
         self.k, self.v, self.page_table = k, v, page_table
         self.device, self.dtype, self.heads, self.dim = k.device, k.dtype, k.shape[-2], k.shape[-1]

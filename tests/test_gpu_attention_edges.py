@@ -350,3 +350,13 @@ def test_wide_caps_come_close_to_none():
     # the same exponents but for a rounding of each of their factors, some 2^-22 of at most 8
     assert (lse - lse2).abs().max() <= 2.0 ** -17
     assert (none.float() - wide.float()).abs().max() <= 2.0 ** -10 * none.float().abs().max()
+
+
+@pytest.mark.parametrize("hq", [4, 64])
+def test_one_head_in_either_order_of_tokens_and_heads(hq):
+    b = Batch([300, 77], _last([300, 77], 2), hq, 1, 64, 16, BF)
+    want, lse = b.attention()
+    b.cache = misa.KVCache(b.k, b.v.transpose(1, 2).contiguous().transpose(1, 2), b.table_dev)
+    out, lse2 = b.attention()
+    assert_status_ok()
+    assert torch.equal(out, want) and torch.equal(lse, lse2)

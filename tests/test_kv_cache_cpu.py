@@ -28,3 +28,15 @@ def test_a_page_table_without_entries_stays_a_paged_cache(misa, table):
 
 def test_a_packed_cache_has_no_page_table(misa):
     assert not misa.KVCache(_cuda_like(40, 2, 128)).c.page_table
+
+
+def test_strides_that_nothing_is_multiplied_by_may_differ(misa):
+    """One head: its stride is whatever the view it comes from had."""
+    k = _cuda_like(4, 16, 1, 128)
+    v = _cuda_like(4, 1, 16, 128).transpose(1, 2)
+    assert k.stride() != v.stride()
+    c = misa.KVCache(k, v, torch.zeros(2, 5, dtype=torch.int32)).c
+    assert (c.page_stride, c.token_stride) == (16 * 128, 128)
+    for bad in (_cuda_like(4, 16, 2, 128), _cuda_like(4, 16, 1, 136)[..., :128], _cuda_like(8, 16, 1, 128)[::2]):
+        with pytest.raises(ValueError, match="strides"):
+            misa.KVCache(k, bad, torch.zeros(2, 5, dtype=torch.int32))
