@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         acc[7] = fmaf(f, y.w, acc[7]);
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that saw nothing: zeros
-      const float lse2 = l == 0.f ? -INFINITY : ref + lg2(l);
+      const float lse2 = l == 0.f ? -INFINITY : log_sum<E, 0>(ref, l);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = l == 0.f ? 0.f : acc[j] * inv;
       if (MODE != kSelected && *s_cut && least < s_pos[r])

@@ -159,6 +159,14 @@ __device__ __forceinline__ float reference(float m) {
   return m;
 }
 
+// The logarithm of a row's sum l, taken from such a reference.  What fp16's weights
+// are raised by is taken out first: lg2's error grows with its result.
+template <typename E, int kAbove>
+__device__ __forceinline__ float log_sum(float ref, float l) {
+  if constexpr (std::is_same<E, __half>::value) return (ref + (15 - kAbove)) + lg2(l * (1.f / (1 << (15 - kAbove))));
+  return ref + lg2(l);
+}
+
 // Row of the cache seen as [map_rows, D], head 0, or -1: place `off` of page `pg`, or, packed,
 // token `pos` of the sequence whose first is `first`.
 __device__ __forceinline__ int cache_unit(const AttendArgs& a, int64_t first, int pos, int pg, int off) {

@@ -510,7 +510,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
       float fa, fb = 0.f, lse2;
       if constexpr (PAIR) {
         fa = l == 0.f ? 0.f : 1.f / l;
-        lse2 = l == 0.f ? -INFINITY : ref + lg2(l);
+        lse2 = l == 0.f ? -INFINITY : log_sum<E, kAbove>(ref, l);
       } else if (s.n == 0) {
         fa = 0.f;  // no keys: nothing to exchange, and the other stream may still read the last item's
         lse2 = -INFINITY;
@@ -531,7 +531,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         const float inv = l == 0.f ? 0.f : 1.f / l;
         fa *= inv;
         fb *= inv;
-        lse2 = l == 0.f ? -INFINITY : base + lg2(l);
+        lse2 = l == 0.f ? -INFINITY : log_sum<E, kAbove>(base, l);
         // stream B's O is complete when its thread came to the barrier, A's likewise
         tc_fence_after();
       }

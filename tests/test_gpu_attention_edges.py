@@ -360,3 +360,24 @@ def test_one_head_in_either_order_of_tokens_and_heads(hq):
     out, lse2 = b.attention()
     assert_status_ok()
     assert torch.equal(out, want) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("hq", [4, 48])                # warp-level and tcgen05 kernels
+def test_lse_of_equal_scores_in_fp16(hq):
+    """Scores of 0: lse is the logarithm of the number of tokens.  Held near log2 of it, 9 to 15.7, where a step is 2^-20:
+    half one for lg2, joining and conversion each, and lg2's own error of as much: under 2^-20 on average over many
+    numbers; 15 above that, where a step is twice as large, every other one was off by more."""
+    lens = [int(n) for n in np.random.default_rng(2).integers(600, 50000, 64)]
+    n = max(lens)
+    pages = -(-n // 64)
+    k = torch.zeros(pages, 64, 1, 64, dtype=FP, device="cuda")
+    prob = misa.Problem(lens, range(65), [x - 1 for x in lens], num_heads=1, block=64)
+    cache = misa.KVCache(k, torch.ones_like(k), torch.arange(pages, dtype=torch.int32, device="cuda").repeat(64, 1))
+    q = torch.zeros(64, hq, 64, dtype=FP, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(64, hq, device="cuda")
+    ws = torch.empty(misa.attention_workspace_size(prob, cache, hq), dtype=torch.uint8, device="cuda")
+    misa.attention(prob, cache, q, out, ws, lse=lse)
+    assert_status_ok()
+    assert (out == 1).all()
+    err = (lse.double().cpu() - torch.tensor(lens).double().log()[:, None]).abs()
+    assert err.max() <= 3 * 2.0 ** -20 and err.mean() <= 2.0 ** -21, (float(err.mean()), float(err.max()))
