@@ -271,8 +271,8 @@ typedef struct {
  *     x = scale * (q . k[s]);   softcap > 0: x = softcap * tanh(x / softcap);
  *     slopes != NULL: x -= slopes[head] * (q_pos[t] - s).
  * An x of -inf counts as masked; a NaN reaches the row's output, and no other
- * row's.  A cap up to 64 puts x off by at most 2^-20 softcap, a larger one by at
- * most 3 2^-20 |x|, however large: a cap far above the scores is as none. */
+ * row's.  A cap puts x off by at most 3 2^-20 |x|, however large it is: one far
+ * above the scores is as none. */
 typedef struct {
   float scale;
   float softcap;                 /* 0: none, else any finite value > 0 */

@@ -368,26 +368,24 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         group_sync<WM>(grp);
       }
       if constexpr (KIND == kCapped) {
-        // four values of one row, of two neighbouring key blocks: what is not a number stays in its row
+        float most = 0.f;
 #pragma unroll
-        for (int n = 0; n < kNT; n += 2) {
+        for (int n = 0; n < kNT; ++n) {
           if (mask) {
-#pragma unroll
-            for (int j = n; j < n + 2; ++j) {
-              const int2 kp = *reinterpret_cast<const int2*>(keys + st * KB + j * 8 + (lane & 3) * 2);
-              if (kp.x < 0 || kp.x > pos0) s[j][0] = 0.f;
-              if (kp.y < 0 || kp.y > pos0) s[j][1] = 0.f;
-              if (kp.x < 0 || kp.x > pos1) s[j][2] = 0.f;
-              if (kp.y < 0 || kp.y > pos1) s[j][3] = 0.f;
-            }
+            const int2 kp = *reinterpret_cast<const int2*>(keys + st * KB + n * 8 + (lane & 3) * 2);
+            if (kp.x < 0 || kp.x > pos0) s[n][0] = 0.f;
+            if (kp.y < 0 || kp.y > pos0) s[n][1] = 0.f;
+            if (kp.x < 0 || kp.x > pos1) s[n][2] = 0.f;
+            if (kp.y < 0 || kp.y > pos1) s[n][3] = 0.f;
           }
-          if (a.wide) {
+          most = max3_abs(max3_abs(most, s[n][0], s[n][1]), s[n][2], s[n][3]);
+        }
+        if (__all_sync(0xffffffffu, most < a.series_max)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) cap_wide(s[n + (j >> 2)][j & 3], a);
-          } else {
-            cap4(s[n][0], s[n][1], s[n + 1][0], s[n + 1][1], a);
-            cap4(s[n][2], s[n][3], s[n + 1][2], s[n + 1][3], a);
-          }
+          for (int j = 0; j < 2 * kNT; ++j) cap_series(s[j >> 1][(j & 1) * 2], s[j >> 1][(j & 1) * 2 + 1], a);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2 * kNT; ++j) cap_any(s[j >> 1][(j & 1) * 2], s[j >> 1][(j & 1) * 2 + 1], a);
         }
       }
 #pragma unroll
@@ -935,8 +933,11 @@ int attend(const misa_problem_t* p, const misa_kv_cache_t* c, const void* q, int
   const double log2e = 1.4426950408889634, raw2 = opts->scale * log2e;
   a.raw2 = finite(raw2, FLT_MAX);
   a.scale2 = cap ? finite(2 * raw2 / opts->softcap, FLT_MAX) : a.raw2;
-  a.cap2 = cap ? finite(opts->softcap * log2e, FLT_MAX / 4) : 0.f;
-  a.wide = opts->softcap > kWideCap;
+  if (cap) {
+    a.cap2 = finite(opts->softcap * log2e, FLT_MAX / 4);
+    a.inv_cap2 = finite(1 / (opts->softcap * log2e), FLT_MAX);
+    a.series_max = finite(raw2 == 0 ? FLT_MAX : kSeries * opts->softcap * log2e / fabs(raw2), FLT_MAX);
+  }
   const RowGrid grid = row_grid(p, c);
   if (grid.rows) {
     // a stride that nothing is multiplied by need not be a multiple of the unit

@@ -28,8 +28,9 @@ struct AttendArgs {
   uint32_t* status;
   float scale2;        // no cap: scale * log2(e); cap: 2 * scale / cap * log2(e)
   float cap2;          // cap * log2(e), or 0
-  float raw2;          // scale * log2(e), for a wide cap
-  int wide;            // the cap is past kWideCap
+  float raw2;          // scale * log2(e)
+  float inv_cap2;      // 1 / cap2
+  float series_max;    // products below this go by the series of tanh: see cap_series
   int S, T, Hq, Hkv, G, k, ng, max_shared, max_seq_len;
   int chunk, nch_max;  // keys of an item; most items along the keys
   int64_t unit;        // the tensor core kernel's rows: elements between them (divides every stride),
@@ -62,17 +63,19 @@ __device__ __forceinline__ float rcp(float x) {
   return r;
 }
 
-// What is done to a product before the softmax, a kernel each: a cap's two
-// more special-function results per element would otherwise be paid by all.
-// A cap past kWideCap is a kind of its own on tcgen05, where the mere presence of
-// its code costs ordinary caps 14 of 150 us (the prefix of 64 sequences behind
-// 32768 shared); the warp-level kernel branches, for 0.3 of 7 (64 lists of 256).
-enum Change { kScaled = 0, kBiased = 1, kCapped = 2 /* and a bias, if there are slopes */, kWideCapped = 3 };
+// What is done to a product before the softmax, a kernel each: a cap's dozen
+// more operations per element would otherwise be paid by all.
+enum Change { kScaled = 0, kBiased = 1, kCapped = 2 /* and a bias, if there are slopes */ };
 
 // Three-way maximum; NaN if any is.
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+__device__ __forceinline__ float max3_abs(float x, float y, float z) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 // Pairs of fp32 values in one 64-bit register pair, for the packed instructions.
@@ -106,43 +109,44 @@ __device__ __forceinline__ float min_nan(float x, float y) {
   return r;
 }
 
-// Four products -> capped exponents of 2.  cap tanh(u) is formed as
-// cap - 2 cap / (e^{2u} + 1): exact at both ends, and off by up to 2^-20 of the
-// cap between, where tanh.approx would be off by 2^-11.  The four quotients
-// share one reciprocal (1 / x = y z w / (x y z w)); e^{2u} is held at 2^30 (tanh
-// is 1 to fp32 from 2^26 on), so that the product stays in range.  A NaN makes
-// all four NaN, so they are four of one row, whose result it makes NaN anyway;
-// places that the row does not see are set to 0 before.
-__device__ __forceinline__ void cap4(float& x0, float& x1, float& x2, float& x3, const AttendArgs& a) {
-  const uint64_t sc = pair(a.scale2, a.scale2), one = pair(1.f, 1.f), c = pair(a.cap2, a.cap2);
-  float y0, y1, y2, y3, m0, m1;
-  unpair(mul2(pair(x0, x1), sc), y0, y1);
-  unpair(mul2(pair(x2, x3), sc), y2, y3);
-  const uint64_t e01 = add2(pair(ex2(min_nan(y0, 30.f)), ex2(min_nan(y1, 30.f))), one);
-  const uint64_t e23 = add2(pair(ex2(min_nan(y2, 30.f)), ex2(min_nan(y3, 30.f))), one);
-  unpair(mul2(e01, e23), m0, m1);
-  const float r = rcp(m0 * m1) * (-2.f * a.cap2);
-  const uint64_t q = pair(r * m1, r * m0);  // -2 cap / (e0 e2), -2 cap / (e1 e3)
-  unpair(fma2(q, e23, c), x0, x1);
-  unpair(fma2(q, e01, c), x2, x3);
+// Products -> capped exponents of 2: cap tanh(u), u = product scale / cap.
+// Below |u| = 1/2, where scores nearly always are, y + y u^2 t(u^2) of the
+// uncapped exponent y, no special function: off by a few roundings of y itself,
+// whatever the cap.  t is the polynomial of four terms that is nearest to
+// (tanh(u) / u - 1) / u^2 there (tanh(u) to 2^-25.9, fitted by least squares with
+// weights that grow with the error).  A warp goes by it where all its products of
+// 32 keys (on tcgen05; of a block's keys otherwise) are below, else by cap_any: 64
+// sequences behind 32768 shared take 244 us, 307 with a score past half the cap in
+// every 32; by quotients of four to a reciprocal alone, off by 2^-20 of the cap, 241.
+constexpr float kSeries = 0.5f;
+__device__ __forceinline__ constexpr float tanh_term(int i) {
+  constexpr float c[4] = {-0.333331435918808f, 0.13325878977775574f, -0.05304549261927605f, 0.01724149100482464f};
+  return c[i];
 }
-
-// The same for a cap past kWideCap, from which on 2^-20 of the cap (6e-5 of an
-// exponent at 64) would show: where |u| < 0.35 the product times tanh(u) / u by
-// its Taylor series to u^10 (off by 2^-24), else the quotient, so that the error
-// is a share of the score, whatever the cap: 2^-21, and 3 2^-20 from the
-// quotient.  Ordinary caps keep cap4: 239 us where this takes 313 (64 sequences
-// behind 32768 shared).
-constexpr float kWideCap = 64.f;
-__device__ __forceinline__ void cap_wide(float& x, const AttendArgs& a) {
-  const float y = x * a.scale2, u = y * (0.5f * kLn2), w = u * u;
-  float t = fmaf(w, -1382.f / 155925.f, 62.f / 2835.f);
-  t = fmaf(w, t, -17.f / 315.f);
-  t = fmaf(w, t, 2.f / 15.f);
-  t = fmaf(w, t, -1.f / 3.f);
-  t = fmaf(w, t, 1.f);
-  const float q = fmaf(-2.f * a.cap2, rcp(ex2(min_nan(y, 30.f)) + 1.f), a.cap2);
-  x = fabsf(u) < 0.35f ? x * a.raw2 * t : q;
+__device__ __forceinline__ uint64_t cap_near(uint64_t x, const AttendArgs& a) {
+  const uint64_t y = mul2(x, pair(a.raw2, a.raw2)), u = mul2(y, pair(a.inv_cap2, a.inv_cap2)), w = mul2(u, u);
+  uint64_t t = pair(tanh_term(3), tanh_term(3));
+#pragma unroll
+  for (int i = 2; i >= 0; --i) t = fma2(w, t, pair(tanh_term(i), tanh_term(i)));
+  return fma2(mul2(y, w), t, y);
+}
+__device__ __forceinline__ void cap_series(float& x0, float& x1, const AttendArgs& a) {
+  unpair(cap_near(pair(x0, x1), a), x0, x1);
+}
+// Any two products of one row: the same, to the bit, below series_max, and
+// cap - 2 cap / (e^{2u} + 1) beyond, exact at both ends and off by up to 2^-20 of
+// the cap between (near 0 that would be more than the score).  The two quotients
+// share a reciprocal (1 / x = y / (x y)), so a NaN of one may reach the other but
+// no other row; e^{2u} is held at 2^60, so that the product stays in range.
+// Places that a row does not see hold 0 here.
+__device__ __forceinline__ void cap_any(float& x0, float& x1, const AttendArgs& a) {
+  float n0, n1, y0, y1, e0, e1;
+  unpair(cap_near(pair(x0, x1), a), n0, n1);
+  unpair(mul2(pair(x0, x1), pair(a.scale2, a.scale2)), y0, y1);
+  unpair(add2(pair(ex2(min_nan(y0, 60.f)), ex2(min_nan(y1, 60.f))), pair(1.f, 1.f)), e0, e1);
+  const float r = rcp(e0 * e1) * (-2.f * a.cap2);
+  x0 = fabsf(x0) < a.series_max ? n0 : fmaf(r, e1, a.cap2);
+  x1 = fabsf(x1) < a.series_max ? n1 : fmaf(r, e0, a.cap2);
 }
 
 // What a row's exponents are taken from, given its maximum (or, on tcgen05, what

@@ -346,7 +346,7 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
         if (lane == 0) mbar_arrive(q_full);
       }
       float slope = 0.f;
-      const bool bias = KIND == kBiased || (KIND >= kCapped && a.slopes);
+      const bool bias = KIND == kBiased || (KIND == kCapped && a.slopes);
       if (a.slopes && bias) slope = __ldg(a.slopes + h) * kLog2e;
       const float sc = KIND == kScaled ? a.scale2 : 1.f;
       // contiguous keys: the last one that this row sees
@@ -383,18 +383,21 @@ attend_tc_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ T
             for (int j = 0; j < 32; ++j)
               if ((MODE != kSelected && j > last - q * 32) || (word >> j & 1u)) u[j] = value;
           };
-          if constexpr (KIND >= kCapped) {
+          if constexpr (KIND == kCapped) {
             mask(0.f);
-            if constexpr (KIND == kWideCapped) {
+            float most = 0.f;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) cap_wide(u[j], a);
+            for (int j = 0; j < 32; j += 2) most = max3_abs(most, u[j], u[j + 1]);
+            if (__all_sync(0xffffffffu, most < a.series_max)) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) cap_series(u[j], u[j + 1], a);
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) cap4(u[j], u[j + 1], u[j + 2], u[j + 3], a);
+              for (int j = 0; j < 32; j += 2) cap_any(u[j], u[j + 1], a);
             }
           }
           if (bias) {
-            const uint64_t mul = KIND >= kCapped ? pair(1.f, 1.f) : pair(a.scale2, a.scale2);
+            const uint64_t mul = KIND == kCapped ? pair(1.f, 1.f) : pair(a.scale2, a.scale2);
             const float* far = s_far + keep * kTile + q * 32;
             const float first = -slope * (float)(pos - base - q * 32);
             const uint64_t step = pair(2.f * slope, 2.f * slope), minus = pair(-slope, -slope);
@@ -887,8 +890,7 @@ int launch_tc_one(const AttendArgs& a, const TcMaps& maps, int64_t bound, cudaSt
 template <typename E, int D, int MODE, bool PAIR>
 int launch_tc_kind(const AttendArgs& a, const TcMaps& m, int64_t bound, cudaStream_t st) {
   // the scaled form takes the maximum before it scales: a scale that is not positive goes to the biased one
-  return a.cap2 > 0.f && a.wide               ? launch_tc_one<E, D, MODE, PAIR, kWideCapped>(a, m, bound, st)
-         : a.cap2 > 0.f                       ? launch_tc_one<E, D, MODE, PAIR, kCapped>(a, m, bound, st)
+  return a.cap2 > 0.f                         ? launch_tc_one<E, D, MODE, PAIR, kCapped>(a, m, bound, st)
          : a.slopes || !(a.scale2 > 0.f) ? launch_tc_one<E, D, MODE, PAIR, kBiased>(a, m, bound, st)
                                               : launch_tc_one<E, D, MODE, PAIR, kScaled>(a, m, bound, st);
 }

@@ -172,7 +172,7 @@ def _check_cap(b, out, lse, idx=None, rows=None, softcap=0.0, scale=None, slopes
     makes no error larger), 2^-20 (max |x| + 1) for the bias, the exponential and the joining, and for
     the cap itself by a share of |x|: its series by 8 roundings (2^-21); its quotient 2 cap / (e + 1),
     at most 2 cap, by 8 roundings and the exponential's 2^-22, so 2^-20 cap in all, where |x| is at least
-    cap tanh(0.35) = 0.336 cap: 3 2^-20 |x|.  Together under 2^-18 (max |x| + 1)."""
+    cap tanh(1/2) = 0.46 cap: 3 2^-20 |x|.  Together under 2^-18 (max |x| + 1)."""
     from oracle import attention as plain
     from tests.attention_cases import HALF_STEP
     u = HALF_STEP[b.dtype]
@@ -381,3 +381,29 @@ def test_lse_of_equal_scores_in_fp16(hq):
     assert (out == 1).all()
     err = (lse.double().cpu() - torch.tensor(lens).double().log()[:, None]).abs()
     assert err.max() <= 3 * 2.0 ** -20 and err.mean() <= 2.0 ** -21, (float(err.mean()), float(err.max()))
+
+
+@pytest.mark.parametrize("softcap", [15.0, 20.0, 30.0, 50.0, 64.0, 300.0])
+@pytest.mark.parametrize("hq", [4, 48])                # warp-level and tcgen05 kernels
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_a_capped_score_is_off_by_a_share_of_itself(softcap, hq, dt):
+    """One token a sequence, so that lse is its score; the products are exact.
+
+    Below half the cap eight roundings of the score (2^-21) and lse's conversion of two (2^-23); beyond, the
+    quotient's share of 2^-20 of the cap, at most twice 2^-20 of the score / tanh(1/2) = 0.46.  fp16's weight, 2^15, is
+    off by half a step of 15 (2^-21) and the exponential's 2^-22, its logarithm by as much again: under 2^-19."""
+    S = 200
+    b = Batch([1] * S, [[0]] * S, hq, 1, 64, 16, dt)
+    b.q.zero_()
+    b.q[:, :, 0] = 8.0                                   # times the scale of 1/8: the score is the key's first element
+    g = torch.Generator().manual_seed(1)
+    x = torch.cat([torch.randn(S // 2, generator=g) * 3, (torch.rand(S // 2, generator=g) - 0.5) * 3 * softcap]).to(dt)
+    for s in range(S):
+        b.k[int(b.table[s, 0]), 0, 0] = 0
+        b.k[int(b.table[s, 0]), 0, 0, 0] = x[s]
+    want = softcap * np.tanh(x.double().numpy() / softcap)
+    tol = 2.0 ** -20 * np.abs(want) * np.where(np.abs(x.double().numpy()) < softcap / 2, 1, 2 / 0.46) + (2.0 ** -19 if dt == FP else 0)
+    for out, lse in (b.attention(softcap=softcap), b.selected(np.zeros((S, 1), np.int32), softcap=softcap)):
+        assert_status_ok()
+        err = np.abs(lse.double().cpu().numpy() - want[:, None])
+        assert (err <= tol[:, None]).all(), f"{(err / tol[:, None]).max():.2f} x its bound"
