@@ -252,7 +252,12 @@ enum { MISA_BF16 = 0, MISA_FP16 = 1 };
  *   not read.
  * k and v are 16-byte aligned; strides are multiples of 8 elements.  A page
  * number outside 0..num_pages-1, or a token past pages_per_seq * page_size
- * (past total_keys, packed), sets MISA_STATUS_BOUNDS and is skipped. */
+ * (past total_keys, packed), sets MISA_STATUS_BOUNDS and is skipped.
+ * Attention over many rows a key head runs on the 5th-generation tensor cores
+ * where the greatest common divisor of the strides (of axes longer than one) is
+ * at least head_dim and the cache spans fewer than 2^31 such steps; any other
+ * layout, such as pages a few elements apart, gives the same results by the
+ * warp-level kernel: 2 x 1000 queries behind 16384 tokens in 2.2 ms, not 0.5. */
 typedef struct {
   void* k;
   void* v;                       /* NULL: keys only (misa_cache_append) */

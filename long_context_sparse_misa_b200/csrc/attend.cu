@@ -17,7 +17,7 @@
 // Own keys may also be cut into equal parts over all blocks (Balance).
 // Bound by HBM where the keys are long (16 sequences of 32768, 8 heads: 231 us,
 // 6.4 TB/s), by the chain of dependent loads and joins where they are short
-// (one of 1000: 9.8 us).  Two blocks an SM, 16-key blocks for heads of 128: the
+// (one of 1000: 10.1 us).  Two blocks an SM, 16-key blocks for heads of 128: the
 // ring's 96 KB keep 64 KB of rows in flight each.
 #include "attend.cuh"
 
@@ -36,7 +36,16 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
-constexpr int kTcRows = 48;  // rows of a unit from which the tcgen05 kernel is used
+// Rows of a unit from which the tcgen05 kernel is used, however few the keys (one
+// sequence, eight key heads of 128, us of this kernel / of tcgen05):
+//   rows    64 keys      128        1024       4096       16384
+//    32    9.0 / 16.5  10 / 11   13 / 16    21 / 19    32 / 30
+//    48   10.4 / 17.9  13 / 12   16 / 17    30 / 21    43 / 31
+//   128   11.5 / 24.1  14 / 17   21 / 24    38 / 28    69 / 37
+//   256   11.5 / 32.4  14 / 26   26 / 37    42 / 40   115 / 53
+// 300 lists of 256: 32 rows 22 / 24, 48 rows 33 / 26; of 2048: 112 / 90, 171 / 91.
+// Below about 1000 keys a rule on the keys too would do better.
+constexpr int kTcRows = 48;
 
 template <int D, int WM, int KB>
 struct Shape {
@@ -786,7 +795,9 @@ void pick_rows(Part& p, int64_t rows, bool grid) {
 // block (512 bytes at 23 GB/s, 22 ns, in the warp-level kernel): the items fill
 // the GPU's places in whole waves, and an item costs its keys and a fixed part;
 // a cluster's join little, partial rows through the workspace a second launch
-// (9 us).  Own keys may instead be balanced over all blocks: no waves.
+// (9 us).  Own keys may instead be balanced over all blocks: no waves.  The costs
+// were measured with heads of 128 and serve heads of 64 unchanged, whose keys are
+// half as long: their fixed parts then count for half of what they are.
 constexpr int kStep = 128;  // keys of a balanced launch's step
 void split_keys(Part& p, int64_t units, int64_t keys, int64_t max_keys, bool clusters, bool balance) {
   const int64_t places = num_sms() * (p.tc ? 1 : 2);

@@ -30,7 +30,7 @@
 // Bound by the chain of one tile (its S, two passes of softmax, P, the product:
 // about 4000 cycles, of which the other stream hides half): 2 x 1000 queries of
 // 32 heads behind 16384 tokens, with a bias, take 503 us (776 TF/s; tensor and
-// special-function pipes 42% busy), 3000 selections of 2048 for 64 heads 520 us.
+// special-function pipes 42% busy), 3000 selections of 2048 for 64 heads 523 us.
 #include <algorithm>
 #include <type_traits>
 

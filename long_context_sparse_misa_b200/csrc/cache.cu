@@ -11,7 +11,7 @@
 // token share through L1.  A thread block takes `tokens` consecutive tokens,
 // about one round of kUnroll items a thread.  What an item reads depends on its
 // number alone, so its loads go out as soon as the block knows how many of its
-// tokens are not padding (one load, 0.1 us of a step of 16 x 3 tokens' 4.1), and
+// tokens are not padding (one load, under 0.1 us of a step of 16 x 3 tokens' 4.1), and
 // the block's warps find each token's sequence, position and cache row (a chain
 // of up to four loads) while they are under way.
 #include "cache.cuh"
